@@ -168,7 +168,7 @@ def prepare(case, seed):
         s.update(k=_rows(gen, sum(n), kv, dim, dt, True), v=_rows(gen, sum(n), kv, dim, dt, False))
     if case["op"] == "decode":
         s.update(q=_rows(gen, len(n), case["heads"], dim, dt, False),
-                 counters=torch.zeros(len(n) * kv, dtype=torch.int32, device="cuda"))
+                 counters=torch.zeros(len(n) * case["heads"], dtype=torch.int32, device="cuda"))
     return s
 
 
