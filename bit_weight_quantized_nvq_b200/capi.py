@@ -33,6 +33,13 @@ class Linear(ctypes.Structure):
                 ("N", _c_i64), ("K", _c_i64)]
 
 
+class KVCache(ctypes.Structure):
+    """``nvq_kv_cache``: the four arrays of a paged Q8_0 cache."""
+    _fields_ = [("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp),
+                ("n_pages", _c_i64), ("n_kv_heads", _c_i64), ("page_size", _c_i64),
+                ("head_dim", _c_i64)]
+
+
 STACK_LINEARS = 7
 
 #: every symbol the C header declares, with (restype, argtypes)
@@ -63,6 +70,17 @@ SIGNATURES = {
                                         _c_i64, _vp, _vp]),
     "nvq_debug_subblock_sums": (ctypes.c_int, [_vp, _vp, ctypes.c_float, _c_i64, _c_i64, _vp,
                                                _vp, _c_i64, _vp, _vp, _vp]),
+    "nvq_kv_write": (ctypes.c_int, [ctypes.POINTER(KVCache), _vp, _c_i64, _vp, _c_i64, ctypes.c_int,
+                                    _vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _vp]),
+    "nvq_kv_read": (ctypes.c_int, [ctypes.POINTER(KVCache), _vp, _c_i64, _vp, _c_i64, ctypes.c_int,
+                                   _vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _vp]),
+    "nvq_attn_decode_workspace_size": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64]),
+    "nvq_attn_decode": (ctypes.c_int, [ctypes.POINTER(KVCache), _vp, _c_i64, ctypes.c_int, _vp, _vp,
+                                       _c_i64, _c_i64, _c_i64, ctypes.c_float, _vp, _c_i64, _vp,
+                                       _vp, ctypes.c_size_t, _vp]),
+    "nvq_attn_prefill": (ctypes.c_int, [_vp, _c_i64, _vp, _c_i64, _vp, _c_i64, ctypes.c_int, _vp,
+                                        _vp, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64,
+                                        ctypes.c_float, ctypes.c_int, _vp, _c_i64, _vp]),
     "nvq_error_flags": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint), ctypes.c_int]),
     "nvq_debug_stalled_wait": (ctypes.c_int, [ctypes.c_uint64, _vp, _vp]),
     "nvq_decoder_stack": (ctypes.c_int, [ctypes.POINTER(Linear), _c_i64, _vp, _c_i64,
@@ -321,9 +339,192 @@ def debug_subblock_sums(codes: torch.Tensor, scales: torch.Tensor, g: float, q: 
     return y, isum
 
 
+#: NVQ_F32, NVQ_F16, NVQ_BF16
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _dtype(t: torch.Tensor) -> int:
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"float32, float16 or bfloat16 expected, not {t.dtype}")
+    return code
+
+
+def _rows(name: str, t: torch.Tensor, heads: int, dim: int, like: torch.Tensor | None = None) -> int:
+    """Elements between the rows of t [rows, heads, dim], whose rows must be
+    contiguous; on the device and of the type of `like`."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name}: [rows, {heads}, {dim}] expected, not {tuple(t.shape)}")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    if like is not None and (t.device != like.device or t.dtype != like.dtype):
+        raise ValueError(f"{name}: {like.dtype} on {like.device} expected")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _index(name: str, t: torch.Tensor, like: torch.Tensor, *shape: int) -> None:
+    if t.dtype != torch.int32 or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous int32 on {like.device} expected")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {shape} expected, not {tuple(t.shape)}")
+
+
+def _cache(cache, like: torch.Tensor) -> KVCache:
+    """The C descriptor of (k_codes, k_scales, v_codes, v_scales)."""
+    kc, ks, vc, vs = cache
+    if kc.dim() != 4 or ks.shape != kc.shape[:3] + (kc.shape[3] // 32,):
+        raise ValueError("cache: codes [pages, kv_heads, page_size, head_dim] and scales "
+                         "[pages, kv_heads, page_size, head_dim / 32] expected")
+    if vc.shape != kc.shape or vs.shape != ks.shape:
+        raise ValueError("cache: keys and values differ in shape")
+    for t, dt in ((kc, torch.int8), (ks, torch.float16), (vc, torch.int8), (vs, torch.float16)):
+        if t.dtype != dt or t.device != like.device or not t.is_contiguous():
+            raise ValueError(f"cache: contiguous int8 codes and float16 scales on {like.device} expected")
+    return KVCache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), *kc.shape)
+
+
+def _batch(cache, like, cu_seqlens, seq_lens, block_table):
+    B = seq_lens.shape[0]
+    max_pages = block_table.shape[-1]
+    _index("seq_lens", seq_lens, like, B)
+    _index("block_table", block_table, like, B, max_pages)
+    if cu_seqlens is not None:
+        _index("cu_seqlens", cu_seqlens, like, B + 1)
+    return B, max_pages
+
+
+def kv_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device="cuda"):
+    """An empty paged Q8_0 cache: (k_codes, k_scales, v_codes, v_scales),
+    codes int8 [n_pages, n_kv_heads, page_size, head_dim] and scales float16
+    [n_pages, n_kv_heads, page_size, head_dim / 32]."""
+    shape = (n_pages, n_kv_heads, page_size, head_dim)
+    codes = [torch.zeros(shape, dtype=torch.int8, device=device) for _ in range(2)]
+    scales = [torch.zeros(shape[:3] + (head_dim // 32,), dtype=torch.float16, device=device)
+              for _ in range(2)]
+    return codes[0], scales[0], codes[1], scales[1]
+
+
+def kv_write(cache, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+             seq_lens: torch.Tensor, block_table: torch.Tensor, stream=None) -> None:
+    """Quantise the rows k, v [rows, n_kv_heads, head_dim] (float32, float16
+    or bfloat16; packed by sequence, the last positions of each) into the
+    cache's pages (nvq_kv_write).  cu_seqlens int32 [B + 1], seq_lens int32
+    [B] (these rows included), block_table int32 [B, max_pages]."""
+    dt = _dtype(k)
+    c = _cache(cache, k)
+    ks = _rows("k", k, c.n_kv_heads, c.head_dim)
+    vs = _rows("v", v, c.n_kv_heads, c.head_dim, k)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("v: as many rows as k expected")
+    B, max_pages = _batch(cache, k, cu_seqlens, seq_lens, block_table)
+    with torch.cuda.device(k.device):
+        _check("nvq_kv_write", _lib.nvq_kv_write(
+            ctypes.byref(c), _ptr(k), ks, _ptr(v), vs, dt, _ptr(cu_seqlens), _ptr(seq_lens),
+            _ptr(block_table), B, max_pages, k.shape[0], _stream(stream)))
+
+
+def kv_read(cache, cu_seqlens: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
+            rows: int, dtype: torch.dtype = torch.float16, k: torch.Tensor | None = None,
+            v: torch.Tensor | None = None, stream=None):
+    """Rows of the cache (nvq_kv_read): the last cu_seqlens[b+1] -
+    cu_seqlens[b] positions of each sequence, packed; returns (k, v) of
+    [rows, n_kv_heads, head_dim].  rows >= cu_seqlens[B]; rows behind the
+    last sequence are left as they were."""
+    c = _cache(cache, cache[0])
+    dev = cache[0].device
+    shape = (rows, c.n_kv_heads, c.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=dev)
+    if v is None:
+        v = torch.empty(shape, dtype=k.dtype, device=dev)
+    dt = _dtype(k)
+    ks = _rows("k", k, c.n_kv_heads, c.head_dim)
+    vs = _rows("v", v, c.n_kv_heads, c.head_dim, k)
+    if k.shape[0] != rows or v.shape[0] != rows or k.device != dev:
+        raise ValueError(f"k, v: {rows} rows on {dev} expected")
+    B, max_pages = _batch(cache, k, cu_seqlens, seq_lens, block_table)
+    with torch.cuda.device(dev):
+        _check("nvq_kv_read", _lib.nvq_kv_read(
+            ctypes.byref(c), _ptr(k), ks, _ptr(v), vs, dt, _ptr(cu_seqlens), _ptr(seq_lens),
+            _ptr(block_table), B, max_pages, rows, _stream(stream)))
+    return k, v
+
+
+def attn_decode(cache, q: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
+                counters: torch.Tensor, scale: float | None = None,
+                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence over the cache
+    (nvq_attn_decode): q [B, n_heads, head_dim] float32, float16 or bfloat16;
+    returns out of q's shape and type.  counters: device int32
+    [B * n_heads], zero before the first call, left zero; calls that may
+    overlap need their own.  scale: 1/sqrt(head_dim) unless given."""
+    dt = _dtype(q)
+    c = _cache(cache, q)
+    B, max_pages = _batch(cache, q, None, seq_lens, block_table)
+    H, D = q.shape[1], c.head_dim
+    qs = _rows("q", q, H, D)
+    if q.shape[0] != B:
+        raise ValueError(f"q: {B} rows expected, one per sequence")
+    if counters.dtype != torch.int32 or counters.device != q.device or not counters.is_contiguous() \
+            or counters.numel() < B * H:
+        raise ValueError(f"counters: contiguous int32 [{B * H}] on {q.device} expected")
+    if out is None:
+        out = torch.empty((B, H, D), dtype=q.dtype, device=q.device)
+    os_ = _rows("out", out, H, D, q)
+    if out.shape[0] != B:
+        raise ValueError(f"out: {B} rows expected")
+    with torch.cuda.device(q.device):
+        if workspace is None:
+            nbytes = int(_lib.nvq_attn_decode_workspace_size(B, H, c.n_kv_heads, D))
+            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+        _check("nvq_attn_decode", _lib.nvq_attn_decode(
+            ctypes.byref(c), _ptr(q), qs, dt, _ptr(seq_lens), _ptr(block_table), B, max_pages,
+            H, float(D ** -0.5 if scale is None else scale), _ptr(out), os_, _ptr(counters),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                 cu_k: torch.Tensor | None = None, scale: float | None = None,
+                 causal: bool = True, out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """Attention of packed prompts (nvq_attn_prefill): q [total_q, n_heads,
+    head_dim], k and v [total_k, n_kv_heads, head_dim], float16 or bfloat16;
+    cu_q, cu_k int32 [B + 1] (cu_k: cu_q unless given); returns out of q's
+    shape and type, rows from cu_q[B] on left as they were."""
+    dt = _dtype(q)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k: [rows, heads, head_dim] expected")
+    H, D = q.shape[1], q.shape[2]
+    Hk = k.shape[1]
+    if cu_k is None:
+        cu_k = cu_q
+    qs = _rows("q", q, H, D)
+    ks = _rows("k", k, Hk, D, q)
+    vs = _rows("v", v, Hk, D, q)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("v: as many rows as k expected")
+    B = cu_q.shape[0] - 1
+    _index("cu_q", cu_q, q, B + 1)
+    _index("cu_k", cu_k, q, B + 1)
+    if out is None:
+        out = torch.empty((q.shape[0], H, D), dtype=q.dtype, device=q.device)
+    os_ = _rows("out", out, H, D, q)
+    if out.shape[0] != q.shape[0]:
+        raise ValueError(f"out: {q.shape[0]} rows expected")
+    with torch.cuda.device(q.device):
+        _check("nvq_attn_prefill", _lib.nvq_attn_prefill(
+            _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, dt, _ptr(cu_q), _ptr(cu_k), B, q.shape[0],
+            k.shape[0], H, Hk, D, float(D ** -0.5 if scale is None else scale), 1 if causal else 0,
+            _ptr(out), os_, _stream(stream)))
+    return out
+
+
 FLAG_GEMV_TIMEOUT = 1
 FLAG_GEMM_TIMEOUT = 2
 FLAG_BAD_INDEX = 4
+FLAG_ATTN_TIMEOUT = 8
 
 
 def error_flags(clear: bool = False) -> int:

@@ -78,6 +78,61 @@ nvq_status check_dot_args(const void* codes, const void* scales, int64_t N,
   return NVQ_OK;
 }
 
+constexpr int64_t kInt32Max = INT32_MAX;
+
+int64_t dtype_bytes(int dtype) {
+  return dtype == NVQ_F32 ? 4 : dtype == NVQ_F16 || dtype == NVQ_BF16 ? 2 : 0;
+}
+
+// A packed tensor of `rows` rows of `width` elements, `stride` apart.
+nvq_status check_rows(const void* p, int64_t rows, int64_t width, int64_t stride, int64_t bytes) {
+  if (rows == 0) return NVQ_OK;
+  if (!p) return NVQ_ERR_INVALID_ARG;
+  if (stride < width || stride > (int64_t{1} << 40)) return NVQ_ERR_BAD_SHAPE;
+  if (!aligned16(p) || stride * bytes % 16 != 0) return NVQ_ERR_MISALIGNED;
+  return NVQ_OK;
+}
+
+nvq_status check_heads(int64_t heads, int64_t kv_heads, int64_t head_dim) {
+  if (heads <= 0 || kv_heads <= 0) return NVQ_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return NVQ_ERR_BAD_SHAPE;
+  if (heads > 65535 || kv_heads > 65535 || heads % kv_heads != 0) return NVQ_ERR_BAD_SHAPE;
+  return NVQ_OK;
+}
+
+nvq_status check_cache(const nvq_kv_cache* c) {
+  if (!c || !c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return NVQ_ERR_INVALID_ARG;
+  if (c->n_pages <= 0 || c->page_size <= 0) return NVQ_ERR_INVALID_ARG;
+  nvq_status st = check_heads(c->n_kv_heads, c->n_kv_heads, c->head_dim);
+  if (st != NVQ_OK) return st;
+  if (c->page_size % 16 != 0 || c->page_size > 65536 || c->n_pages > kInt32Max ||
+      c->n_pages * c->n_kv_heads > kInt32Max / c->page_size)   // rows are 32-bit coordinates
+    return NVQ_ERR_BAD_SHAPE;
+  if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) ||
+      !aligned16(c->v_scales))
+    return NVQ_ERR_MISALIGNED;
+  return NVQ_OK;
+}
+
+// The packed batch of nvq_kv_write and nvq_kv_read.  The index arrays hold
+// int32 and need only their own alignment.
+nvq_status check_kv(const nvq_kv_cache* c, const void* k, int64_t k_stride, const void* v,
+                    int64_t v_stride, int dtype, const int32_t* cu, const int32_t* lens,
+                    const int32_t* table, int64_t B, int64_t max_pages, int64_t rows) {
+  if (B < 0 || max_pages < 0 || rows < 0 || dtype_bytes(dtype) == 0) return NVQ_ERR_INVALID_ARG;
+  nvq_status st = check_cache(c);
+  if (st != NVQ_OK) return st;
+  if (B > kInt32Max - 1 || max_pages > kInt32Max || rows > kInt32Max) return NVQ_ERR_BAD_SHAPE;
+  if (B == 0 || rows == 0) return NVQ_OK;
+  if (!cu || !lens || (!table && max_pages > 0)) return NVQ_ERR_INVALID_ARG;
+  const int64_t width = c->n_kv_heads * c->head_dim;
+  st = check_rows(k, rows, width, k_stride, dtype_bytes(dtype));
+  if (st != NVQ_OK) return st;
+  return check_rows(v, rows, width, v_stride, dtype_bytes(dtype));
+}
+
+bool good_scale(float scale) { return scale > 0.0f && scale <= 3.0e38f; }
+
 }  // namespace
 
 namespace nvq {
@@ -344,6 +399,95 @@ nvq_status nvq_debug_subblock_sums(const uint8_t* codes, const uint8_t* scales, 
                                            static_cast<cudaStream_t>(stream)));
 }
 
+nvq_status nvq_kv_write(const nvq_kv_cache* cache, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, int dtype, const int32_t* cu_seqlens,
+                        const int32_t* seq_lens, const int32_t* block_table, int64_t B,
+                        int64_t max_pages, int64_t rows, void* stream) {
+  nvq_status st = check_kv(cache, k, k_stride, v, v_stride, dtype, cu_seqlens, seq_lens,
+                           block_table, B, max_pages, rows);
+  if (st != NVQ_OK || B == 0 || rows == 0) return st;
+  st = check_device();
+  if (st != NVQ_OK) return st;
+  const nvq::KvBatch b = {cu_seqlens, seq_lens, block_table, B, max_pages, rows};
+  return cuda_status(nvq::launch_kv_write(*cache, b, k, k_stride, v, v_stride, dtype,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+nvq_status nvq_kv_read(const nvq_kv_cache* cache, void* k, int64_t k_stride, void* v,
+                       int64_t v_stride, int dtype, const int32_t* cu_seqlens,
+                       const int32_t* seq_lens, const int32_t* block_table, int64_t B,
+                       int64_t max_pages, int64_t rows, void* stream) {
+  nvq_status st = check_kv(cache, k, k_stride, v, v_stride, dtype, cu_seqlens, seq_lens,
+                           block_table, B, max_pages, rows);
+  if (st != NVQ_OK || B == 0 || rows == 0) return st;
+  st = check_device();
+  if (st != NVQ_OK) return st;
+  const nvq::KvBatch b = {cu_seqlens, seq_lens, block_table, B, max_pages, rows};
+  return cuda_status(nvq::launch_kv_read(*cache, b, k, k_stride, v, v_stride, dtype,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+size_t nvq_attn_decode_workspace_size(int64_t B, int64_t n_heads, int64_t n_kv_heads,
+                                      int64_t head_dim) {
+  if (B <= 0 || check_heads(n_heads, n_kv_heads, head_dim) != NVQ_OK) return 0;
+  return nvq::attn_decode_workspace_size(B, n_heads, n_kv_heads, head_dim);
+}
+
+nvq_status nvq_attn_decode(const nvq_kv_cache* cache, const void* q, int64_t q_stride, int dtype,
+                           const int32_t* seq_lens, const int32_t* block_table, int64_t B,
+                           int64_t max_pages, int64_t n_heads, float scale, void* out,
+                           int64_t out_stride, int32_t* counters, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (B < 0 || max_pages < 0 || dtype_bytes(dtype) == 0 || !good_scale(scale))
+    return NVQ_ERR_INVALID_ARG;
+  nvq_status st = check_cache(cache);
+  if (st != NVQ_OK) return st;
+  st = check_heads(n_heads, cache->n_kv_heads, cache->head_dim);
+  if (st != NVQ_OK) return st;
+  if (B > 65535 || max_pages > kInt32Max || max_pages * cache->page_size > kInt32Max)
+    return NVQ_ERR_BAD_SHAPE;
+  if (B == 0) return NVQ_OK;
+  if (!seq_lens || (!block_table && max_pages > 0) || !counters) return NVQ_ERR_INVALID_ARG;
+  const int64_t width = n_heads * cache->head_dim;
+  st = check_rows(q, B, width, q_stride, dtype_bytes(dtype));
+  if (st == NVQ_OK) st = check_rows(out, B, width, out_stride, dtype_bytes(dtype));
+  if (st != NVQ_OK) return st;
+  if (!workspace || workspace_bytes < nvq::attn_decode_workspace_size(B, n_heads, cache->n_kv_heads,
+                                                                      cache->head_dim))
+    return NVQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return NVQ_ERR_MISALIGNED;
+  st = check_device();
+  if (st != NVQ_OK) return st;
+  return cuda_status(nvq::launch_attn_decode(*cache, seq_lens, block_table, B, max_pages, q,
+                                             q_stride, n_heads, scale, dtype, out, out_stride,
+                                             counters, workspace,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+nvq_status nvq_attn_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, int dtype, const int32_t* cu_q,
+                            const int32_t* cu_k, int64_t B, int64_t total_q, int64_t total_k,
+                            int64_t n_heads, int64_t n_kv_heads, int64_t head_dim, float scale,
+                            int causal, void* out, int64_t out_stride, void* stream) {
+  if (B < 0 || total_q < 0 || total_k < 0 || !good_scale(scale)) return NVQ_ERR_INVALID_ARG;
+  if (dtype != NVQ_F16 && dtype != NVQ_BF16) return NVQ_ERR_INVALID_ARG;
+  nvq_status st = check_heads(n_heads, n_kv_heads, head_dim);
+  if (st != NVQ_OK) return st;
+  if (B > 65535 || total_q > kInt32Max / 2 || total_k > kInt32Max / 2) return NVQ_ERR_BAD_SHAPE;
+  if (B == 0 || total_q == 0) return NVQ_OK;
+  if (!cu_q || !cu_k) return NVQ_ERR_INVALID_ARG;
+  st = check_rows(q, total_q, n_heads * head_dim, q_stride, 2);
+  if (st == NVQ_OK) st = check_rows(out, total_q, n_heads * head_dim, out_stride, 2);
+  if (st == NVQ_OK) st = check_rows(k, total_k, n_kv_heads * head_dim, k_stride, 2);
+  if (st == NVQ_OK) st = check_rows(v, total_k, n_kv_heads * head_dim, v_stride, 2);
+  if (st != NVQ_OK) return st;
+  st = check_device();
+  if (st != NVQ_OK) return st;
+  const nvq::PrefillArgs a = {q, k, v, out, q_stride, k_stride, v_stride, out_stride, cu_q, cu_k,
+                              B, total_q, total_k, n_heads, n_kv_heads, head_dim, scale, causal};
+  return cuda_status(nvq::launch_attn_prefill(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+
 nvq_status nvq_error_flags(unsigned int* flags, int clear) {
   if (!flags) return NVQ_ERR_INVALID_ARG;
   nvq_status st = check_device();
@@ -354,12 +498,18 @@ nvq_status nvq_error_flags(unsigned int* flags, int clear) {
   if (e == cudaSuccess) e = nvq::gemm_small_error_flags(clear != 0, &gemm_small);
   if (e == cudaSuccess) e = nvq::nvf4_error_flags(clear != 0, &nvf4);
   gemm |= gemm_small | nvf4;
+  unsigned int kv = 0, decode = 0, prefill = 0;
+  if (e == cudaSuccess) e = nvq::kv_error_flags(clear != 0, &kv);
+  if (e == cudaSuccess) e = nvq::attn_decode_error_flags(clear != 0, &decode);
+  if (e == cudaSuccess) e = nvq::attn_prefill_error_flags(clear != 0, &prefill);
+  const unsigned int attn = kv | decode | prefill;
   if (e != cudaSuccess) {
     cudaGetLastError();
     return cuda_status(e);
   }
   *flags = ((gemv & 1u) ? NVQ_FLAG_GEMV_TIMEOUT : 0u) | (gemm ? NVQ_FLAG_GEMM_TIMEOUT : 0u) |
-           ((gemv & 2u) ? NVQ_FLAG_BAD_INDEX : 0u);
+           (((gemv | attn) & 2u) ? NVQ_FLAG_BAD_INDEX : 0u) |
+           ((attn & 1u) ? NVQ_FLAG_ATTN_TIMEOUT : 0u);
   return NVQ_OK;
 }
 

@@ -8,6 +8,8 @@
 
 #include <cuda_runtime.h>
 
+#include "nvq.h"
+
 namespace nvq {
 
 // Q8_0 activation quantiser over M*K/32 blocks.
@@ -129,6 +131,46 @@ cudaError_t gemm_expand(const int8_t* q, const uint16_t* d, int64_t M, int64_t K
 cudaError_t gemm_main(const uint8_t* codes, const uint8_t* scales, float g, int64_t N,
                       int64_t K, int64_t M, float* y, const void* workspace,
                       cudaStream_t stream);
+
+// Paged Q8_0 cache: the packed batch whose rows are written or read (row r
+// of sequence b is position seq_lens[b] - cu_seqlens[b + 1] + r).
+struct KvBatch {
+  const int32_t* cu_seqlens;
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  int64_t B, max_pages, rows;
+};
+cudaError_t launch_kv_write(const nvq_kv_cache& c, const KvBatch& b, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride, int dtype,
+                            cudaStream_t stream);
+cudaError_t launch_kv_read(const nvq_kv_cache& c, const KvBatch& b, void* k, int64_t k_stride,
+                           void* v, int64_t v_stride, int dtype, cudaStream_t stream);
+cudaError_t kv_error_flags(bool clear, unsigned int* flags);
+
+// Attention of one new token per sequence over the paged cache.
+size_t attn_decode_workspace_size(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim);
+cudaError_t launch_attn_decode(const nvq_kv_cache& c, const int32_t* seq_lens,
+                               const int32_t* block_table, int64_t B, int64_t max_pages,
+                               const void* q, int64_t q_stride, int64_t heads, float scale,
+                               int dtype, void* out, int64_t out_stride, int32_t* counters,
+                               void* workspace, cudaStream_t stream);
+cudaError_t attn_decode_error_flags(bool clear, unsigned int* flags);
+
+// Attention of packed prompts (fp16 or bf16).
+struct PrefillArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int64_t B, total_q, total_k, heads, kv_heads, head_dim;
+  float scale;
+  int causal;
+};
+cudaError_t launch_attn_prefill(const PrefillArgs& a, int dtype, cudaStream_t stream);
+cudaError_t attn_prefill_error_flags(bool clear, unsigned int* flags);
 
 // The allocation-free GEMM: bytes of its library-owned scratch, and the
 // scratch's device address on the current device (looked up once per

@@ -395,10 +395,151 @@ nvq_status nvq_debug_subblock_sums(const uint8_t* codes, const uint8_t* scales, 
                                    int64_t N, int64_t K, const int8_t* q, const uint16_t* d,
                                    int64_t M, float* y, int32_t* isum, void* stream);
 
+/* Element types of the cache's rows and of the attention operands. */
+#define NVQ_F32  0
+#define NVQ_F16  1
+#define NVQ_BF16 2
+
+/*
+ * A paged key-value cache in Q8_0, in device memory owned by the caller.
+ * Page p holds page_size tokens of every key-value head:
+ *   k_codes, v_codes    int8   [n_pages, n_kv_heads, page_size, head_dim]
+ *   k_scales, v_scales  uint16 [n_pages, n_kv_heads, page_size, head_dim/32]
+ *                       (fp16 bits), one per 32 values along the head.
+ * head_dim is 64 or 128, page_size a multiple of 16 up to 65536; all four
+ * arrays 16-byte aligned.  The values are those of nvq_quantize_act_q8_0.
+ *
+ * A batch of B sequences is described by int32 device arrays:
+ *   block_table [B, max_pages]  the pages of each sequence, in order;
+ *   seq_lens [B]                tokens in the cache of each sequence, those
+ *                               of the current call included;
+ *   cu_seqlens [B + 1]          rows of the packed tensors: sequence b has
+ *                               rows cu_seqlens[b] .. cu_seqlens[b+1] - 1,
+ *                               cu_seqlens[0] = 0, never decreasing.
+ * Entries of block_table behind a sequence's last page are not read.  A
+ * length or a page outside its range never reads or writes outside the
+ * arrays; it raises NVQ_FLAG_BAD_INDEX.
+ */
+typedef struct nvq_kv_cache {
+  int8_t* k_codes;
+  uint16_t* k_scales;
+  int8_t* v_codes;
+  uint16_t* v_scales;
+  int64_t n_pages, n_kv_heads, page_size, head_dim;
+} nvq_kv_cache;
+
+/*
+ * nvq_kv_write - quantise new keys and values into the cache's pages.
+ *
+ * k, v  device rows [rows, n_kv_heads, head_dim] of `dtype` (NVQ_F32,
+ *       NVQ_F16, NVQ_BF16), finite; k_stride and v_stride are the elements
+ *       from one row to the next (>= n_kv_heads * head_dim, a multiple of 16
+ *       bytes), so slices of a fused projection's output can be passed.
+ * Row r of sequence b becomes position seq_lens[b] - (cu_seqlens[b+1] - r):
+ * the packed rows are the sequence's last positions.  Rows from
+ * cu_seqlens[B] on are padding and are not written; nor is a row whose
+ * position is negative or whose page is bad, which raises
+ * NVQ_FLAG_BAD_INDEX.  Codes and scales are bit-identical to
+ * nvq_quantize_act_q8_0 of the rows as fp32.  A page that is written must
+ * belong to one sequence of the call (pages shared by a common prefix are
+ * read, not written): two rows written to one place leave either's values.
+ * Errors: NVQ_ERR_INVALID_ARG (NULL, negative sizes, unknown dtype),
+ * NVQ_ERR_BAD_SHAPE (head_dim, page_size, a stride below the row's length,
+ * sizes over 2^31 - 1), NVQ_ERR_MISALIGNED, NVQ_ERR_UNSUPPORTED_DEVICE,
+ * NVQ_ERR_CUDA.
+ */
+nvq_status nvq_kv_write(const nvq_kv_cache* cache, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, int dtype,
+                        const int32_t* cu_seqlens, const int32_t* seq_lens,
+                        const int32_t* block_table, int64_t B, int64_t max_pages,
+                        int64_t rows, void* stream);
+
+/*
+ * nvq_kv_read - read rows of the cache back as packed fp32, fp16 or bf16.
+ *
+ * k, v  device rows [rows, n_kv_heads, head_dim] of `dtype`: outputs, with
+ *       strides as in nvq_kv_write.  Row r of sequence b is position
+ *       seq_lens[b] - (cu_seqlens[b+1] - r): the whole context where
+ *       cu_seqlens has seq_lens' sums, the rows just written with the
+ *       arguments of the write.  Values are fp16(d) * q, exact in fp32 and
+ *       rounded once to fp16 or bf16.  Rows from cu_seqlens[B] on, and rows
+ *       without a valid place (NVQ_FLAG_BAD_INDEX), are left as they were.
+ * Errors: as nvq_kv_write.
+ */
+nvq_status nvq_kv_read(const nvq_kv_cache* cache, void* k, int64_t k_stride, void* v,
+                       int64_t v_stride, int dtype, const int32_t* cu_seqlens,
+                       const int32_t* seq_lens, const int32_t* block_table, int64_t B,
+                       int64_t max_pages, int64_t rows, void* stream);
+
+/*
+ * nvq_attn_decode - attention of one new token per sequence over the cache
+ * (the token's own key and value already written).
+ *
+ * q     device rows [B, n_heads, head_dim] of `dtype`, q_stride elements
+ *       from one sequence to the next; n_heads a multiple of n_kv_heads,
+ *       head h reads key-value head h / (n_heads / n_kv_heads).
+ * out   device rows [B, n_heads, head_dim] of `dtype`, out_stride elements
+ *       apart: sum_j p_j v_j / sum_j p_j, p_j = exp(scale * q.k_j - max), over
+ *       the seq_lens[b] positions of sequence b; zeros where it is 0.
+ * scale finite and > 0 (customarily 1/sqrt(head_dim)).
+ * Products, softmax statistics and sums are fp32; with NVQ_F32 the operands
+ * of the products carry at least 22 bits, with the 16-bit types the
+ * probabilities are rounded to tf32 (fp16's significand, fp32's range) for the
+ * product with the values.
+ * A length over max_pages * page_size is cut there, a negative one counts as
+ * 0, a bad page reads page 0; each raises NVQ_FLAG_BAD_INDEX.
+ * counters  device int32 [B * n_heads], 0 before the first call; every
+ *           call leaves them 0.
+ * workspace device scratch of nvq_attn_decode_workspace_size(...) bytes.
+ *           Calls that may run at the same time need their own counters and
+ *           workspace.  Results do not depend on timing.
+ * Errors: as nvq_kv_write, NVQ_ERR_WORKSPACE, NVQ_ERR_INVALID_ARG for a
+ * scale that is not finite and positive, NVQ_ERR_BAD_SHAPE when n_heads is no
+ * multiple of n_kv_heads.
+ */
+nvq_status nvq_attn_decode(const nvq_kv_cache* cache, const void* q, int64_t q_stride,
+                           int dtype, const int32_t* seq_lens, const int32_t* block_table,
+                           int64_t B, int64_t max_pages, int64_t n_heads, float scale,
+                           void* out, int64_t out_stride, int32_t* counters, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Workspace bytes nvq_attn_decode needs on the current device (0 on bad input). */
+size_t nvq_attn_decode_workspace_size(int64_t B, int64_t n_heads, int64_t n_kv_heads,
+                                      int64_t head_dim);
+
+/*
+ * nvq_attn_prefill - attention of packed prompts of different lengths.
+ *
+ * q    device rows [total_q, n_heads, head_dim], k and v device rows
+ *      [total_k, n_kv_heads, head_dim], out device rows [total_q, n_heads,
+ *      head_dim], all of `dtype` (NVQ_F16 or NVQ_BF16); *_stride elements
+ *      from one row to the next (multiples of 16 bytes).  head_dim is 64 or
+ *      128; n_heads a multiple of n_kv_heads.
+ * cu_q, cu_k  device int32 [B + 1]: rows of sequence b in q/out and in k/v,
+ *      each starting at 0, never decreasing.  With n queries and m keys,
+ *      query i sees the keys j < m, if `causal` only j <= i + m - n (the
+ *      queries are the last n positions, so a prefix read back from the
+ *      cache goes in front).  A query that sees no key gives zeros.
+ * Keys and values that a query does not see do not reach it, whatever they
+ * hold (NaN and infinities included).  Rows of out from cu_q[B] on are left
+ * as they were.  Products accumulate in fp32, softmax statistics are fp32,
+ * the probabilities are rounded to `dtype` for the product with the values.
+ * A row range outside total_q or total_k raises NVQ_FLAG_BAD_INDEX; the
+ * sequence counts as having no keys, its rows inside total_q give zeros.
+ * Errors: as nvq_attn_decode; NVQ_ERR_INVALID_ARG for another dtype.
+ */
+nvq_status nvq_attn_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, int dtype, const int32_t* cu_q,
+                            const int32_t* cu_k, int64_t B, int64_t total_q, int64_t total_k,
+                            int64_t n_heads, int64_t n_kv_heads, int64_t head_dim, float scale,
+                            int causal, void* out, int64_t out_stride, void* stream);
+
 /* Bits of nvq_error_flags. */
 #define NVQ_FLAG_GEMV_TIMEOUT 1u  /* a GEMV pipeline wait gave up (4 s)  */
 #define NVQ_FLAG_GEMM_TIMEOUT 2u  /* a GEMM pipeline wait gave up (4 s)  */
-#define NVQ_FLAG_BAD_INDEX    4u  /* nvq_moe_gemv met a routing id outside 0..E-1 */
+#define NVQ_FLAG_BAD_INDEX    4u  /* nvq_moe_gemv met a routing id outside 0..E-1, or a
+                                     cache or attention call a bad length or page */
+#define NVQ_FLAG_ATTN_TIMEOUT 8u  /* an attention pipeline wait gave up (4 s) */
 
 /*
  * nvq_error_flags - device-side error flags of the current device.

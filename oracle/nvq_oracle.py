@@ -80,6 +80,7 @@ __all__ = [
     "y_from_subblock_sums", "sum_abs_terms", "tolerance",
     "dot_fp64_f16", "sum_abs_terms_f16", "moe_dot_fp64",
     "quantize_act_nvfp4", "dot_fp64_nvf4", "sum_abs_terms_nvf4",
+    "attend_fp64",
     "ACC_REL_TOL", "ACC_ABS_TOL",
 ]
 
@@ -520,3 +521,40 @@ def sum_abs_terms_nvf4(w_codes, w_scales, w_g, a_codes, a_scales, a_g) -> np.nda
                   for m in range(np.asarray(a_codes).shape[0])])
     w = dequantize_weights(w_codes, w_scales, w_g)
     return np.abs(a) @ np.abs(w).T
+
+
+# ---------------------------------------------------------------------------
+# Attention over keys and values
+# ---------------------------------------------------------------------------
+
+def attend_fp64(q, k, v, scale: float, causal: bool = True):
+    """Attention of one sequence in fp64: q [n, H, D], k and v [m, Hkv, D]
+    (head h reads key-value head h // (H // Hkv)); query i sees the keys
+    j < m, with `causal` only j <= i + m - n:
+
+        o[i, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q_i.k_j - max).
+
+    A query that sees no key gives zeros.  A key or value that a query does
+    not see does not enter its sums.  Returns (o [n, H, D], a [n, H, D] =
+    sum_j p_j |v_j| / sum_j p_j, e [n, H] = scale * max_j sum_d |q_d k_jd|),
+    the last two being what an error bound is stated in.
+    Pinned by tests/test_oracle_attention.py."""
+    q, k, v = (np.asarray(x, dtype=np.float64) for x in (q, k, v))
+    n, H, D = q.shape
+    m, Hkv = k.shape[:2]
+    o = np.zeros((n, H, D))
+    a = np.zeros((n, H, D))
+    e = np.zeros((n, H))
+    for h in range(H):
+        kh, vh = k[:, h // (H // Hkv)], v[:, h // (H // Hkv)]
+        for i in range(n):
+            end = min(m, i + m - n + 1) if causal else m
+            if end <= 0:
+                continue
+            s = scale * (kh[:end] @ q[i, h])
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            o[i, h] = p @ vh[:end]
+            a[i, h] = p @ np.abs(vh[:end])
+            e[i, h] = scale * (np.abs(kh[:end]) @ np.abs(q[i, h])).max()
+    return o, a, e

@@ -1,0 +1,212 @@
+"""Prompt attention of packed sequences against the oracle, every element,
+within the bounds that tests/attention_ref.py derives."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as o
+from attention_ref import Cache, bound, check, cu_of
+from bit_weight_quantized_nvq_b200 import capi, workloads as wl
+from parity import Packed
+
+pytestmark = pytest.mark.gpu
+
+
+def rows(n, h, d, dtype, seed, gain=1.0):
+    x = np.random.default_rng(seed).standard_normal((n, h, d)).astype(np.float32) * gain
+    return torch.from_numpy(x).to(dtype).cuda()
+
+
+def compare(q, k, v, n, m, out, dtype, causal, scale=None, what=""):
+    i = j = 0
+    dim = q.shape[2]
+    for b, (a, c) in enumerate(zip(n, m)):
+        args = [x.double().cpu().numpy() for x in (q[i:i + a], k[j:j + c], v[j:j + c])]
+        ref, aa, e = o.attend_fp64(*args, dim ** -0.5 if scale is None else scale, causal)
+        vmax = np.abs(args[2]).max() if c else 0.0
+        check(out[i:i + a], ref, bound(ref, aa, e, c, vmax, dtype, dtype), f"{what} sequence {b} ({a}, {c})")
+        i, j = i + a, j + c
+
+
+CASES = [  # kv heads, group, dim, queries, keys
+    (1, 1, 64, [1], [1]), (1, 1, 128, [128], [128]), (2, 2, 128, [1, 5, 127, 129], [1, 5, 127, 129]),
+    (1, 3, 64, [300, 0, 17], [300, 0, 17]), (2, 5, 128, [33, 200], [500, 257]), (1, 8, 64, [1, 1, 1], [700, 128, 129]),
+    (4, 1, 128, [257, 1], [257, 64]), (1, 2, 64, [10, 4, 0, 6], [3, 0, 9, 6]), (1, 4, 128, [130, 260], [100, 259]),
+    (1, 16, 64, [70], [70])]
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("kv,group,dim,n,m", CASES)
+def test_prefill_matches_the_oracle(dtype, causal, kv, group, dim, n, m):
+    H, N, M = kv * group, sum(n), sum(m)
+    pad = 3                                                  # rows behind the last sequence
+    fq = rows(N + pad, H + 2, dim, dtype, 1)                 # slices of fused projections
+    fkv = rows(M + pad, 2 * kv + 1, dim, dtype, 2)
+    fq[N:], fkv[M:] = float("nan"), float("nan")
+    q, k, v = fq[:, 2:], fkv[:, :kv], fkv[:, kv + 1:]
+    out = torch.full((N + pad, H + 1, dim), 3.0, dtype=dtype, device="cuda")
+    capi.attn_prefill(q, k, v, cu_of(n), cu_of(m), causal=causal, out=out[:, :H])
+    torch.cuda.synchronize()
+    compare(q, k, v, n, m, out[:N, :H], dtype, causal)
+    assert (out[N:] == 3).all() and (out[:, H] == 3).all()
+    assert capi.error_flags() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_rows_that_peak_late_and_early(dtype, dim):
+    """The running maximum grows by much at late keys, falls, or stays; large
+    and small scores and scales."""
+    n = 700
+    q, k, v = rows(n, 2, dim, dtype, 1), rows(n, 1, dim, dtype, 2), rows(n, 1, dim, dtype, 3)
+    ramp = torch.linspace(0, 6, n, device="cuda").view(-1, 1, 1).to(dtype)
+    for kk in (k * ramp, k * ramp.flip(0), k * 0, k):
+        for scale in (0.02, 0.5):
+            out = capi.attn_prefill(q, kk.contiguous(), v, cu_of([n]), scale=scale)
+            compare(q, kk, v, [n], [n], out, dtype, True, scale)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim,kv,group", [(128, 1, 2), (64, 2, 1), (128, 1, 1)])
+def test_what_a_query_does_not_see_does_not_reach_it(dtype, dim, kv, group):
+    """NaN and infinities in later keys and values of the same sequence, in
+    other sequences, and behind the last one."""
+    n = [150, 90, 300]
+    N = sum(n)
+    q, k, v = rows(N, kv * group, dim, dtype, 1), rows(N + 5, kv, dim, dtype, 2), rows(N + 5, kv, dim, dtype, 3)
+    clean = capi.attn_prefill(q, k, v, cu_of(n), cu_of(n))
+    compare(q, k, v, n, n, clean, dtype, True)
+    for where, bad in ((100, float("nan")), (149, float("inf")), (150 + 60, float("-inf")), (240 + 130, float("nan")),
+                       (240 + 257, float("inf")), (N + 1, float("nan"))):
+        for in_v in (True, False):
+            kk, vv = k.clone(), v.clone()
+            if in_v:
+                vv[where, :, 3::7] = bad
+            else:
+                kk[where] = float("nan")
+            out = capi.attn_prefill(q, kk, vv, cu_of(n), cu_of(n))
+            torch.cuda.synchronize()
+            hit = torch.zeros(N, dtype=torch.bool)
+            at = 0
+            for a in n:
+                if at <= where < at + a:
+                    hit[where:at + a] = True
+                at += a
+            hit = hit.cuda()
+            # the same tiles and the same order of sums: bit-identical where nothing is seen
+            assert torch.equal(out[~hit], clean[~hit]), (where, bad, in_v)
+            if in_v and hit.any():
+                got = out[hit].float()
+                cols = torch.zeros(dim, dtype=torch.bool)
+                cols[3::7] = True
+                assert torch.equal(out[hit][..., ~cols.cuda()], clean[hit][..., ~cols.cuda()])
+                seen = got[..., cols.cuda()]
+                # a weight that rounds to zero makes 0 * inf of an infinity
+                assert (torch.isnan(seen) | torch.isinf(seen)).all()
+                if bad != bad:
+                    assert torch.isnan(seen).all()
+            elif hit.any():
+                assert torch.isnan(out[hit].float()).all()
+
+
+def test_long_and_ragged_sampled_rows():
+    """Several blocks of queries and keys in either direction, sampled."""
+    n, m, H, kv, dim = [1100, 37, 2049], [1500, 400, 2049], 6, 2, 128
+    q, k, v = rows(sum(n), H, dim, torch.bfloat16, 1), rows(sum(m), kv, dim, torch.bfloat16, 2), rows(sum(m), kv, dim, torch.bfloat16, 3)
+    out = capi.attn_prefill(q, k, v, cu_of(n), cu_of(m))
+    torch.cuda.synchronize()
+    i = j = 0
+    rng = np.random.default_rng(0)
+    for a, c in zip(n, m):
+        kh, vh = k[j:j + c].double().cpu().numpy(), v[j:j + c].double().cpu().numpy()
+        for r in sorted({0, a - 1, *rng.integers(0, a, 12).tolist()}):
+            end = r + c - a + 1
+            ref, aa, e = o.attend_fp64(q[i + r:i + r + 1].double().cpu().numpy(), kh[:end], vh[:end], dim ** -0.5)
+            check(out[i + r:i + r + 1], ref, bound(ref, aa, e, end, np.abs(vh).max(), torch.bfloat16, torch.bfloat16), f"row {r}")
+        i, j = i + a, j + c
+    for _ in range(3):
+        assert torch.equal(capi.attn_prefill(q, k, v, cu_of(n), cu_of(m)), out)
+
+
+def test_many_sequences():
+    rng = np.random.default_rng(4)
+    n = np.where(rng.random(1050) < 0.3, 0, rng.integers(1, 9, 1050)).tolist()
+    q, k, v = rows(sum(n), 2, 64, torch.float16, 1), rows(sum(n), 1, 64, torch.float16, 2), rows(sum(n), 1, 64, torch.float16, 3)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = capi.attn_prefill(q, k, v, cu_of(n), stream=side)
+    torch.cuda.synchronize()
+    compare(q, k, v, n, n, out, torch.float16, True)
+
+
+def test_a_captured_call_follows_its_inputs():
+    N = 300
+    q, k, v = rows(N, 4, 128, torch.float16, 1), rows(N, 2, 128, torch.float16, 2), rows(N, 2, 128, torch.float16, 3)
+    cu = cu_of([100, 200])
+    out = capi.attn_prefill(q, k, v, cu)
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        capi.attn_prefill(q, k, v, cu, out=out)
+    for n in ([300, 0], [1, 299], [130, 130]):
+        cu.copy_(cu_of(n))
+        q.copy_(rows(N, 4, 128, torch.float16, n[0]))
+        out.fill_(2)
+        graph.replay()
+        torch.cuda.synchronize()
+        compare(q, k, v, n, n, out, torch.float16, True)
+        assert (out[sum(n):] == 2).all()
+
+
+def test_bad_ranges_stay_inside_and_are_flagged():
+    capi.error_flags(clear=True)
+    q, k, v = rows(40, 2, 64, torch.float16, 1), rows(40, 1, 64, torch.float16, 2), rows(40, 1, 64, torch.float16, 3)
+    good = capi.attn_prefill(q, k, v, cu_of([10, 30]))
+    for cu_q, cu_k in (([0, 10, 40], [0, 10, 50]), ([0, 10, 40], [0, 10, 5]), ([0, 10, 40], [0, 10, -7]), ([0, 10, 45], [0, 10, 40])):
+        out = torch.full_like(q, 9)
+        capi.attn_prefill(q, k, v, torch.tensor(cu_q, dtype=torch.int32).cuda(), torch.tensor(cu_k, dtype=torch.int32).cuda(), out=out)
+        torch.cuda.synchronize()
+        assert capi.error_flags(clear=True) == capi.FLAG_BAD_INDEX, (cu_q, cu_k)
+        assert torch.equal(out[:10], good[:10]) and not out[10:40].any()
+    # no keys at all
+    empty = torch.empty((0, 1, 64), dtype=torch.float16, device="cuda")
+    out = capi.attn_prefill(q, empty, empty, cu_of([10, 30]), cu_of([0, 0]))
+    assert not out.any() and capi.error_flags() == 0
+
+
+def test_prompt_chain():
+    """A prompt in two chunks as it is used: projections, cache write, the
+    context read back, attention, output projection."""
+    hidden, H, kv, D = 512, 8, 2, 64
+    Ps = {name: Packed(wl.weights("attn_chain", name, n, hidden)) for name, n in (("q", H * D), ("k", kv * D), ("v", kv * D))}
+    po = Packed(wl.weights("attn_chain", "o", hidden, H * D))
+    page, chunks = 16, [(50, 20), (70, 33)]
+    cache = capi.kv_cache(16, kv, page, D)
+    table = torch.from_numpy(np.random.default_rng(1).permutation(16).reshape(2, 8).astype(np.int32)).cuda()
+    done = [0, 0]
+    for step, new in enumerate(chunks):
+        x = torch.from_numpy(wl.activations("attn_chain", f"p{step}", sum(new), hidden)).cuda()
+        xq, xd = capi.quantize_act_q8_0(x)
+        y = {name: capi.gemm(P.codes, P.scales, P.g, xq, xd) for name, P in Ps.items()}
+        lens = [a + b for a, b in zip(done, new)]
+        ln = torch.tensor(lens, dtype=torch.int32).cuda()
+        capi.kv_write(cache, y["k"].view(-1, kv, D), y["v"].view(-1, kv, D), cu_of(new), ln, table)
+        k, v = capi.kv_read(cache, cu_of(lens), ln, table, sum(lens))
+        q = y["q"].view(-1, H, D).half()
+        att = capi.attn_prefill(q, k, v, cu_of(new), cu_of(lens))
+        aq, ad = capi.quantize_act_q8_0(att.float().view(-1, H * D))
+        out = capi.gemm(po.codes, po.scales, po.g, aq, ad)
+        torch.cuda.synchronize()
+        compare(q, k, v, list(new), lens, att, torch.float16, True)
+        # the chunk's own rows are the quantised projections
+        at = lens[0] - new[0]
+        q8, d8 = o.quantize_q8_0(y["k"][: new[0]].cpu().numpy().reshape(-1, D))
+        want = torch.from_numpy(o.dequantize_activations(q8, d8).astype(np.float32)).half()
+        assert torch.equal(k[at:lens[0]].reshape(-1, D).cpu(), want)
+        q8, d8 = o.quantize_q8_0(att.float().view(-1, H * D).cpu().numpy())
+        ref = o.dot_fp64(po.ref_codes, po.ref_scales, po.ref_g, q8, d8)
+        tol = o.tolerance(o.sum_abs_terms(o.subblock_sums(po.ref_codes, q8), po.ref_scales, po.ref_g, d8))
+        assert np.all(np.abs(out.cpu().numpy() - ref) <= tol)
+        done = lens
+    assert capi.error_flags() == 0

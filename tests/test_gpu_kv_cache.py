@@ -1,0 +1,151 @@
+"""The paged Q8_0 cache on the GPU: rows are quantised as written,
+bit-identical to the oracle's Q8_0, and read back exactly (one rounding to
+the 16-bit types); nothing else in the cache or the outputs changes."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as o
+from attention_ref import Cache, cu_of
+from bit_weight_quantized_nvq_b200 import capi
+
+pytestmark = pytest.mark.gpu
+
+
+def rows(n, heads, dim, dtype, seed):
+    x = np.random.default_rng(seed).standard_t(4, (n, heads, dim)).astype(np.float32)
+    if n:
+        x[0, 0, :32] = 0                       # a block of zeros
+        x[-1, -1, -32:] *= 1e-6
+    return torch.from_numpy(x).to(dtype).cuda()
+
+
+def expect_written(cache, b, first, x):
+    """What the oracle's quantiser puts at the positions from `first` on."""
+    n, heads, dim = x.shape
+    q, d = o.quantize_q8_0(x.float().cpu().numpy().reshape(n * heads, dim))
+    return q.reshape(n, heads, dim), d.reshape(n, heads, dim // 32)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("heads,dim,page,new,past", [
+    (8, 128, 64, [1] * 5, [0, 63, 64, 200, 15]), (1, 64, 16, [3, 0, 17, 40], [5, 9, 0, 31]),
+    (3, 64, 48, [1], [0]), (40, 128, 16, [33, 1], [0, 16]), (5, 128, 256, [70, 0, 0, 9], [500, 3, 0, 255])])
+def test_write_then_read(dtype, heads, dim, page, new, past):
+    lens = [n + p for n, p in zip(new, past)]
+    c = Cache(lens, heads, page, dim, seed=3)
+    dev = c.device()
+    before = [t.cpu().clone() for t in dev]
+    n, pad = sum(new), 3
+    fused = torch.cat([rows(n + pad, heads, dim, dtype, 1), rows(n + pad, heads, dim, dtype, 2)], 1)
+    k, v = fused[:, :heads], fused[:, heads:]          # slices of one projection's output
+    cu, ln, table = cu_of(new), c.dev_lens(), c.dev_table()
+    capi.kv_write(dev, k, v, cu, ln, table)
+    torch.cuda.synchronize()
+    want = [t.numpy().copy() for t in before]
+    at = 0
+    for b, (m, first) in enumerate(zip(new, past)):
+        pos = first + np.arange(m)
+        pg, off = c.table[b, pos // page], pos % page
+        for w, x in ((0, k), (2, v)):
+            q, d = expect_written(c, b, first, x[at:at + m])
+            want[w][pg, :, off] = q
+            want[w + 1].view(np.uint16)[pg, :, off] = d
+        at += m
+    for got, ref in zip(dev, want):
+        assert np.array_equal(got.cpu().numpy().view(np.uint8), ref.view(np.uint8))
+    # read back: the rows just written, then whole contexts, into strided outputs with rows to spare
+    for cus in (new, lens):
+        total = sum(cus)
+        for out in (torch.float32, torch.float16, torch.bfloat16):
+            buf = torch.full((total + 2, 2 * heads, dim), 7.0, dtype=out, device="cuda")
+            gk, gv = capi.kv_read(dev, cu_of(cus), ln, table, total + 2, k=buf[:, :heads], v=buf[:, heads:])
+            torch.cuda.synchronize()
+            assert (gk[total:] == 7).all() and (gv[total:] == 7).all()
+            at = 0
+            for b, m in enumerate(cus):
+                pos = lens[b] - m + np.arange(m)
+                pg, off = c.table[b, pos // page], pos % page
+                for w, g in ((0, gk), (2, gv)):
+                    val = want[w][pg, :, off].astype(np.float32) * np.repeat(want[w + 1][pg, :, off].astype(np.float32), 32, -1)
+                    assert torch.equal(g[at:at + m].cpu(), torch.from_numpy(val).to(out))
+                at += m
+    assert capi.error_flags() == 0
+
+
+def test_write_is_the_activation_quantiser():
+    x = rows(37, 4, 128, torch.float32, 9)
+    c = capi.kv_cache(4, 4, 16, 128)
+    table, lens = torch.tensor([[2, 0, 3]], dtype=torch.int32).cuda(), torch.tensor([37], dtype=torch.int32).cuda()
+    capi.kv_write(c, x, x, cu_of([37]), lens, table)
+    q, d = capi.quantize_act_q8_0(x.reshape(37 * 4, 128))
+    pos = torch.arange(37, device="cuda")
+    pg = table[0].long()[pos // 16]
+    for codes, scales in (c[:2], c[2:]):
+        assert torch.equal(codes[pg, :, pos % 16].reshape(-1, 128), q)
+        assert torch.equal(scales[pg, :, pos % 16].reshape(-1, 4), d)
+
+
+def test_bad_lengths_and_pages_are_skipped_and_flagged():
+    capi.error_flags(clear=True)
+    c = capi.kv_cache(3, 2, 16, 64)
+    x = rows(6, 2, 64, torch.float16, 4)
+    cu = cu_of([2, 2, 2])
+    for lens, table in (([1, 2, 2], [[0], [1], [2]]), ([2, 17, 2], [[0], [1], [2]]), ([2, 2, 2], [[0], [3], [2]]),
+                        ([2, 2, 2], [[0], [-1], [2]])):
+        for t in c:
+            t.zero_()
+        ln, tb = (torch.tensor(z, dtype=torch.int32).cuda() for z in (lens, table))
+        capi.kv_write(c, x, x, cu, ln, tb)
+        gk, _ = capi.kv_read(c, cu, ln, tb, 6, k=torch.full_like(x, 5))
+        torch.cuda.synchronize()
+        assert capi.error_flags(clear=True) == capi.FLAG_BAD_INDEX
+        bad = 0 if lens[0] == 1 else 1
+        # a length of 1 for two rows has no place for the first; one over the table none for the second
+        lost = {0: [0], 1: [3] if lens[1] == 17 else [2, 3]}[bad]
+        kept = [r for r in range(6) if r not in lost]
+        assert (gk[lost] == 5).all()
+        assert (gk[kept].float() - x[kept].float()).abs().max() < x.float().abs().max() / 100
+    assert capi.error_flags() == 0
+
+
+def test_offsets_over_32_bits():
+    """Pages whose codes lie beyond 2^31 and 2^32 bytes."""
+    heads, page, dim = 8, 256, 128                       # 256 KiB of codes a page
+    n_pages = (9 << 30) // (2 * heads * page * dim)      # 4.5 GiB for the keys, as much for the values
+    kc = torch.empty((n_pages, heads, page, dim), dtype=torch.int8, device="cuda")
+    ks = torch.empty((n_pages, heads, page, dim // 32), dtype=torch.float16, device="cuda")
+    c = (kc, ks, torch.empty_like(kc), torch.empty_like(ks))
+    table = torch.tensor([[n_pages - 1, 0], [n_pages // 2, n_pages - 2]], dtype=torch.int32).cuda()
+    lens = torch.tensor([300, 260], dtype=torch.int32).cuda()
+    x = rows(560, heads, dim, torch.float32, 6)
+    cu = cu_of([300, 260])
+    capi.kv_write(c, x, x.flip(0), cu, lens, table)
+    k, v = capi.kv_read(c, cu, lens, table, 560, torch.float32)
+    q, d = capi.quantize_act_q8_0(x.reshape(-1, dim))
+    want = (q.float().unflatten(-1, (-1, 32)) * d.float().unsqueeze(-1)).reshape(560, heads, dim)
+    assert torch.equal(k, want) and torch.equal(v, want.flip(0))
+    qs = x[:2].repeat(1, 2, 1)
+    out = capi.attn_decode(c, qs, lens, table, torch.zeros(2 * 16, dtype=torch.int32, device="cuda"))
+    for b, (a, n) in enumerate(((0, 300), (300, 260))):
+        kk, vv = (t[a:a + n].double().repeat_interleave(2, 1) for t in (k, v))
+        p = torch.softmax(torch.einsum("hd,nhd->hn", qs[b].double(), kk) / dim ** 0.5, -1)
+        ref = torch.einsum("hn,nhd->hd", p, vv)
+        assert (out[b].double() - ref).abs().max() < 1e-4 * ref.abs().max()
+
+
+def test_many_sequences_and_another_stream():
+    """A batch over one and two search rounds, mostly of nothing, on a stream of its own."""
+    side = torch.cuda.Stream()
+    for B in (33, 1100):
+        rng = np.random.default_rng(B)
+        lens = np.where(rng.random(B) < 0.5, 0, rng.integers(1, 20, B)).tolist()
+        c = Cache(lens, 2, 16, 64, seed=B)
+        dev = c.device()
+        cu, ln, table = cu_of(lens), c.dev_lens(), c.dev_table()
+        torch.cuda.synchronize()
+        k, v = capi.kv_read(dev, cu, ln, table, sum(lens), torch.float32, stream=side)
+        side.synchronize()
+        want = [np.concatenate([c.values(b)[w] for b in range(B)]) for w in range(2)]
+        assert np.array_equal(k.cpu().numpy(), want[0].astype(np.float32))
+        assert np.array_equal(v.cpu().numpy(), want[1].astype(np.float32))
