@@ -3,102 +3,784 @@
 //   o[h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[h].k_j - m),
 //   m = max_j scale * q[h].k_j,  j < len;  an empty context gives 0.
 //
-// One CTA per (sequence, head).  Each warp takes every fourth token and
-// keeps its own running maximum, sum and output row (online softmax); the
-// four are joined at the end.
+// One pass over the cache with a running maximum and sum.  The floor is the
+// cache's bytes, 2 * 1.0625 per key-value pair of elements, so everything is
+// arranged around the copy stream; what comes next is the instruction issue
+// (int8 to floating point), hence the layouts below.
+//
+// Work split.  A unit is (sequence, key-value head, chunk of the heads that
+// share it); its context is cut into tiles of 64 tokens.  The tiles of all
+// units, in order, are split evenly over a fixed grid of persistent CTAs, so
+// one long sequence and many ragged ones balance alike.  A unit that falls
+// on several CTAs leaves (m, l, o) parts in the workspace; the CTA that
+// arrives last at the unit's counter joins them in the order of the tiles
+// (the result does not depend on timing) and sets the counter back to 0.
+//
+// Copies.  One producer warp moves tiles to shared memory: codes by 2-D TMA
+// (64 rows, or four boxes of 16 where pages end inside a tile), swizzled so
+// that both read patterns below are free of bank conflicts; scales by 1-D bulk
+// copies.  Four consumer warps take 16 tokens of each tile.
+//
+// Scores (m16n8k16, fp16 operands): A holds the queries, B the codes of 8
+// tokens, which are exact in fp16.  Each query row is scaled by a power of
+// two to just below 2^14 before it is rounded, so 16-bit queries are exact
+// and fp32 ones become an exact pair hi + lo of at least 22 bits, in rows g and
+// g + 8 of the same fragment.  Two MMAs cover one block of 32 values; its
+// scale is then applied in fp32.
+//
+// Values (m16n8k8, tf32 operands): the accumulators of the scores are, in the
+// same lanes, the left operand of this product.  A = p_j * scale_j of one
+// 32-block, in tf32 because the scales need fp32's range (fp32 rows: hi + lo
+// again), B = the codes, exact.
+//
+// These are warp-level MMAs: there are at most 16 query rows per key-value
+// head, an eighth of the smallest tcgen05 tile, and the operands change
+// with every tile, so the tensor pipe is not what bounds this kernel.
+#include <algorithm>
+#include <mutex>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
 #include "kv_device.cuh"
+#include "nvq_device.cuh"
 #include "nvq_internal.h"
+#include "tcgen05.cuh"
 
 namespace nvq {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kTile = 64;            // tokens of a tile
+constexpr int kWarps = 4;            // consumer warps, 16 tokens of a tile each
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kConsumers = 32 * kWarps;
+constexpr uint64_t kWaitLimitNs = 4000000000ull;
+constexpr float kLazy = 8.0f;        // the running maximum may lag by this power of two
 
-__device__ unsigned int g_attn_decode_error_flags = 0;   // bit 1: a bad index
+// How the 16 rows of an MMA are used: fp32 heads as hi (rows 0-7) and lo
+// (rows 8-15); up to 8 heads of a 16-bit type; up to 16 of them.
+enum Rows { kSplit = 0, kOne = 1, kTwo = 2 };
+
+__device__ unsigned int g_attn_decode_error_flags = 0;   // bit 0: a wait timed out, bit 1: a bad index
 
 struct DecodeArgs {
-  const int8_t* kc;
   const __half* ks;
-  const int8_t* vc;
   const __half* vs;
   const int32_t* lens;
   const int32_t* table;
-  int max_pages, n_pages, page, kv_heads, heads;
+  const void* q;
+  void* out;
+  int64_t q_stride, out_stride;
+  int* counters;
+  float* part;             // [2 * grid][rows][D + 4]: o, then m and l
+  int B, max_pages, n_pages, page, kv_heads, group, chunks, rows, dtype;
   float scale_log2;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
-attn_decode_kernel(DecodeArgs a, const T* __restrict__ q, int64_t q_stride, T* __restrict__ out,
-                   int64_t out_stride) {
-  constexpr int E = D / 32;            // values of the head per lane, within one Q8_0 block
-  const int b = blockIdx.y, h = blockIdx.x, hk = h / (a.heads / a.kv_heads);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float qv[E], o[E], m = -INFINITY, l = 0.0f;
+template <int D, Rows R>
+struct Cfg {
+  static constexpr int kHeads = R == kTwo ? 16 : 8;          // heads of a chunk
+  static constexpr int kBlocks = D / 32;
+  static constexpr int kStages = 3;
+  static constexpr int kCodes = kTile * D;                   // bytes of a tile's codes
+  static constexpr int kScales = kTile * kBlocks * 2;
+  static constexpr int kRedStride = D + 4;                   // float4 stores of 8 rows hit all banks
+  static constexpr int kOffV = kStages * kCodes;
+  static constexpr int kOffKs = 2 * kStages * kCodes;
+  static constexpr int kOffVs = kOffKs + kStages * kScales;
+  static constexpr int kOffRed = kOffVs + kStages * kScales;
+  static constexpr int kOffMl = kOffRed + kWarps * kHeads * kRedStride * 4;
+  static constexpr int kOffBars = kOffMl + kWarps * kHeads * 8 + kHeads * 4;
+  static constexpr int kSmem = kOffBars + 2 * kStages * 8 + 16 + 1024;
+  static constexpr int kCtas = R == kTwo ? 2 : 3;            // per SM
+};
+
+// Tiles of all units in order: sequence by sequence, unit by unit.
+struct Walk {
+  int b, unit, tile, n;      // position; n: tiles of a unit of sequence b
+  int64_t left;              // tiles of this CTA from here on, this one included
+};
+
+__device__ __forceinline__ int64_t clamp_len(const DecodeArgs& a, int b) {
+  const int64_t len = __ldg(a.lens + b), cap = static_cast<int64_t>(a.max_pages) * a.page;
+  return len < 0 ? 0 : len > cap ? cap : len;
+}
+__device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b) {
+  return static_cast<int>((clamp_len(a, b) + kTile - 1) / kTile);
+}
+
+// Split of W tiles over G CTAs: the first W % G have one more.
+struct Split {
+  int64_t base, rem;
+  __device__ Split(int64_t W, int G) : base(W / G), rem(W % G) {}
+  __device__ int64_t start(int64_t c) const { return c * base + (c < rem ? c : rem); }
+  __device__ int owner(int64_t t) const {
+    const int64_t big = rem * (base + 1);
+    return static_cast<int>(t < big ? t / (base + 1) : rem + (t - big) / base);
+  }
+};
+
+__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    qv[i] = dev::to_f32(q[b * q_stride + h * D + lane * E + i]) * a.scale_log2;
-    o[i] = 0.0f;
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ int64_t warp_scan64(int64_t v, int lane) {   // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
   }
-  int64_t len = a.lens[b];
-  if (len < 0 || len > static_cast<int64_t>(a.max_pages) * a.page) {
-    if (threadIdx.x == 0) atomicOr(&g_attn_decode_error_flags, 2u);
-    len = len < 0 ? 0 : static_cast<int64_t>(a.max_pages) * a.page;
-  }
-  for (int64_t t = warp; t < len; t += kWarps) {
-    int page = a.table[static_cast<int64_t>(b) * a.max_pages + t / a.page];
-    if (page < 0 || page >= a.n_pages) {
-      if (lane == 0) atomicOr(&g_attn_decode_error_flags, 2u);
-      page = 0;
+  return v;
+}
+
+// On to the next sequence with tokens (there is one while tiles are left).
+__device__ __forceinline__ void next_sequence(const DecodeArgs& a, Walk& w) {
+  do {
+    if (++w.b >= a.B) {
+      w.left = 0;
+      return;
     }
-    const int64_t at = ((static_cast<int64_t>(page) * a.kv_heads + hk) * a.page + t % a.page) * D + lane * E;
-    const float dk = __half2float(a.ks[at / 32]), dv = __half2float(a.vs[at / 32]);
-    float s = 0.0f;
+    w.n = tiles_of(a, w.b);
+  } while (w.n == 0);
+}
+__device__ __forceinline__ void advance(const DecodeArgs& a, Walk& w, int U) {
+  if (--w.left <= 0) return;
+  if (++w.tile < w.n) return;
+  w.tile = 0;
+  if (++w.unit < U) return;
+  w.unit = 0;
+  next_sequence(a, w);
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+// Four int8 codes (u = code + 128 per byte) as exact fp16: 0x64bb is 1024 + u.
+__device__ __forceinline__ void codes_to_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));   // 1152
+  lo = dev::h2_bits(__hsub2(dev::bits_h2(__byte_perm(u, 0x64646464u, 0x4140)), bias));
+  hi = dev::h2_bits(__hsub2(dev::bits_h2(__byte_perm(u, 0x64646464u, 0x4342)), bias));
+}
+// The same as fp32: 0x4B0000bb is 2^23 + u.  The sums are exact.
+__device__ __forceinline__ void codes_to_f32(uint32_t w, uint32_t (&f)[4]) {
+  const uint32_t u = w ^ 0x80808080u;
 #pragma unroll
-    for (int i = 0; i < E; ++i) s += qv[i] * static_cast<float>(a.kc[at + i]);
-    s *= dk;
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(m, s), c = exp2f(m - mn), p = exp2f(s - mn);
-    m = mn;
-    l = l * c + p;
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = o[i] * c + p * dv * static_cast<float>(a.vc[at + i]);
+  for (int i = 0; i < 4; ++i)
+    f[i] = __float_as_uint(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + i)) - 8388736.0f);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Eight consecutive elements of a row.
+__device__ __forceinline__ void load8(const void* p, int64_t at, int dtype, float (&x)[8]) {
+  if (dtype == NVQ_F32) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    const float4 u = __ldg(s), v = __ldg(s + 1);
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+    return;
   }
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
+  const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < E; ++i) so[warp][lane * E + i] = o[i];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float M = -INFINITY, L = 0.0f, O = 0.0f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-    for (int w = 0; w < kWarps; ++w) {
-      const float c = sl[w] > 0.0f ? exp2f(sm[w] - M) : 0.0f;
-      L += sl[w] * c;
-      O += so[w][threadIdx.x] * c;
+  for (int i = 0; i < 4; ++i) {
+    if (dtype == NVQ_F16) {
+      const float2 f = __half22float2(dev::bits_h2(w[i]));
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    } else {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
-    out[b * out_stride + h * D + threadIdx.x] = dev::from_f32<T>(len == 0 ? 0.0f : O / L);
+  }
+}
+__device__ __forceinline__ void store4(void* p, int64_t at, int dtype, float4 v) {
+  if (dtype == NVQ_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = v;
+  } else if (dtype == NVQ_F16) {
+    *reinterpret_cast<uint2*>(static_cast<__half*>(p) + at) =
+        make_uint2(dev::h2_bits(__floats2half2_rn(v.x, v.y)), dev::h2_bits(__floats2half2_rn(v.z, v.w)));
+  } else {
+    const __nv_bfloat162 u = __floats2bfloat162_rn(v.x, v.y), w = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&w));
   }
 }
 
-template <typename T>
-cudaError_t decode_t(const nvq_kv_cache& c, const DecodeArgs& a, int64_t B, const void* q,
-                     int64_t q_stride, void* out, int64_t out_stride, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.heads), static_cast<unsigned>(B));
-  if (c.head_dim == 64)
-    attn_decode_kernel<T, 64><<<grid, kWarps * 32, 0, stream>>>(a, static_cast<const T*>(q), q_stride, static_cast<T*>(out), out_stride);
-  else
-    attn_decode_kernel<T, 128><<<grid, kWarps * 32, 0, stream>>>(a, static_cast<const T*>(q), q_stride, static_cast<T*>(out), out_stride);
-  return cudaGetLastError();
+__device__ __forceinline__ void consumer_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+}
+
+// One query row's values of this lane (8 per block: 32 * block + 8 * j ..) as
+// A fragments: scaled by a power of two so that the row's largest lies in
+// [2^13, 2^14), then rounded to fp16, and the remainder for `lo`.  Returns
+// the factor that turns the MMA's sums into powers of two.
+template <int D, bool LO>
+__device__ __forceinline__ float query_row(const DecodeArgs& a, int64_t at, bool on, int j,
+                                           uint32_t (&hi)[D / 8], uint32_t (&lo)[D / 8]) {
+  float x[D / 4], top = 0.0f;
+#pragma unroll
+  for (int bl = 0; bl < D / 32; ++bl) {
+    float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (on) load8(a.q, at + 32 * bl + 8 * j, a.dtype, y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[8 * bl + i] = y[i];
+      top = fmaxf(top, fabsf(y[i]));
+    }
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  // 2^(13 - exponent), kept within fp32's normal range (zeros and subnormals)
+  const int k = min(126, 140 - static_cast<int>(__float_as_uint(top) >> 23));
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    const float u = x[2 * i] * up, v = x[2 * i + 1] * up;
+    const __half2 h = __floats2half2_rn(u, v);
+    hi[i] = dev::h2_bits(h);
+    if (LO) {
+      const float2 f = __half22float2(h);
+      lo[i] = dev::h2_bits(__floats2half2_rn(u - f.x, v - f.y));
+    }
+  }
+  return a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+}
+
+template <int D, Rows R>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, R>::kCtas))
+attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
+                   const __grid_constant__ CUtensorMap v_map, const DecodeArgs a) {
+  using C = Cfg<D, R>;
+  extern __shared__ unsigned char smem_raw[];
+  // the swizzle pattern is a function of the address: tiles on 1024 bytes
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  const uint32_t pad = (1024 - (raw & 1023)) & 1023;
+  unsigned char* smem = smem_raw + pad;
+  const uint32_t base = raw + pad;
+  auto full = [&](int s) { return base + C::kOffBars + 8u * s; };
+  auto empty = [&](int s) { return base + C::kOffBars + 8u * (C::kStages + s); };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBars + 16 * C::kStages);
+  int* last_flag = reinterpret_cast<int*>(smem + C::kOffBars + 16 * C::kStages + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(full(s), 1);
+      ptx::mbar_init(empty(s), kWarps);
+    }
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tensormap(&k_map);
+    ptx::prefetch_tensormap(&v_map);
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  const int U = a.kv_heads * a.chunks;
+  const int G = gridDim.x, cta = blockIdx.x;
+  // every warp finds the CTA's first tile for itself (no hand-over): the sum
+  // of all tiles, then the sequence that holds the first one
+  int64_t total = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) total += b0 + lane < a.B ? tiles_of(a, b0 + lane) : 0;
+  total = warp_sum64(total) * U;
+  const Split split(total, G);
+  const int64_t first = split.start(cta);
+  Walk w = {0, 0, 0, 1, split.start(cta + 1) - first};
+  int64_t unit_start = 0;       // tile number at which the unit of `w` starts
+  if (w.left > 0) {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int64_t mine = b0 + lane < a.B ? tiles_of(a, b0 + lane) : 0;
+      const int64_t incl = warp_scan64(mine, lane);
+      const unsigned hit = __ballot_sync(0xffffffffu, (before + incl) * U > first);
+      if (hit != 0) {
+        const int at = __ffs(hit) - 1;
+        w.b = b0 + at;
+        w.n = static_cast<int>(__shfl_sync(0xffffffffu, mine, at));
+        before += __shfl_sync(0xffffffffu, incl - mine, at);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    const int64_t r = first - before * U;
+    w.unit = static_cast<int>(r / w.n);
+    w.tile = static_cast<int>(r - static_cast<int64_t>(w.unit) * w.n);
+    unit_start = first - w.tile;
+  }
+
+  auto fail = [&]() {
+    *abort_flag = 1;
+    atomicOr(&g_attn_decode_error_flags, 1u);
+  };
+  auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    const bool got = ptx::mbar_wait_bounded(bar, parity, abort_flag, kWaitLimitNs);
+    return __all_sync(0xffffffffu, got);
+  };
+
+  if (warp == kWarps) {
+    // ------------------------------ producer --------------------------------
+    // Lane 4 * i + x copies granule i of array x (codes of K, of V, scales of
+    // K, of V): the whole tile where pages hold whole tiles, else 16 tokens.
+    const int gran = a.page % kTile == 0 ? kTile : 16;
+    const int gi = lane >> 2, arr = lane & 3;
+    int g = 0;
+    bool more = w.left > 0;
+    for (; more; ++g) {
+      const int64_t len = clamp_len(a, w.b);
+      const int valid = static_cast<int>(min(static_cast<int64_t>(kTile), len - static_cast<int64_t>(w.tile) * kTile));
+      const int n = (valid + gran - 1) / gran;        // granules with tokens in them
+      const bool mine = gi < n;
+      int64_t row = 0;
+      if (mine) {
+        const int64_t pos = static_cast<int64_t>(w.tile) * kTile + gi * gran;
+        int page = __ldg(a.table + static_cast<int64_t>(w.b) * a.max_pages + pos / a.page);
+        if (page < 0 || page >= a.n_pages) {
+          atomicOr(&g_attn_decode_error_flags, 2u);
+          page = 0;
+        }
+        row = (static_cast<int64_t>(page) * a.kv_heads + w.unit / a.chunks) * a.page + pos % a.page;
+      }
+      const int s = g % C::kStages;
+      if (!warp_wait(empty(s), ((g / C::kStages) & 1) ^ 1)) {
+        fail();
+        break;
+      }
+      if (lane == 0) ptx::mbar_arrive_expect_tx(full(s), n * gran * (2 * D + 4 * C::kBlocks));
+      __syncwarp();
+      if (mine) {
+        const uint32_t to = base + s * C::kCodes + gi * gran * D;
+        const uint32_t to_s = base + s * C::kScales + gi * gran * 2 * C::kBlocks;
+        if (arr == 0)
+          ptx::tma_load_2d(to, &k_map, 0, static_cast<int>(row), full(s));
+        else if (arr == 1)
+          ptx::tma_load_2d(to + C::kOffV, &v_map, 0, static_cast<int>(row), full(s));
+        else if (arr == 2)
+          ptx::bulk_load(to_s + C::kOffKs, a.ks + row * C::kBlocks, gran * 2 * C::kBlocks, full(s));
+        else
+          ptx::bulk_load(to_s + C::kOffVs, a.vs + row * C::kBlocks, gran * 2 * C::kBlocks, full(s));
+      }
+      __syncwarp();
+      advance(a, w, U);
+      more = w.left > 0;
+    }
+    if (*abort_flag) {
+      // the consumers may have stopped: wait for the copies in flight
+      for (int i = max(0, g - C::kStages); i < g; ++i)
+        ptx::mbar_wait_bounded(full(i % C::kStages), (i / C::kStages) & 1, nullptr, kWaitLimitNs);
+    }
+    return;
+  }
+
+  // -------------------------------- consumers -------------------------------
+  const int gq = lane >> 2, j = lane & 3;
+  // Token order inside a tile of 8: column n of the score MMA is token
+  // perm(n).  It makes the four rows that a half-warp reads (K), and the
+  // four that the lanes j read (V), fall on different banks.
+  constexpr uint32_t kPerm = D == 128 ? 0x57136420u : 0x67235410u;
+  auto perm = [](int n) { return static_cast<int>((kPerm >> (4 * n)) & 7u); };
+  auto swz = [](int r) { return D == 128 ? r : (r >> 1) & 3; };   // chunk xor of row r
+  const int tk = perm(gq), ta = perm(2 * j), tb = perm(2 * j + 1);
+  const uint32_t off_k = (16 * warp + tk) * D + (((j >> 1) ^ swz(tk)) << 4) + (j & 1) * 8;
+  const uint32_t off_va = (16 * warp + ta) * D + (((gq >> 2) ^ swz(ta)) << 4) + (gq & 3) * 4;
+  const uint32_t off_vb = (16 * warp + tb) * D + (((gq >> 2) ^ swz(tb)) << 4) + (gq & 3) * 4;
+  constexpr int kH = R == kTwo ? 2 : 1;      // heads of this lane: gq, and gq + 8
+
+  float* red = reinterpret_cast<float*>(smem + C::kOffRed);
+  float* ml = reinterpret_cast<float*>(smem + C::kOffMl);            // [warp][head][m, l]
+  float* top_s = ml + kWarps * C::kHeads * 2;                        // [head]
+
+  // sequences without tokens: zeros
+  for (int b = cta; b < a.B; b += G) {
+    const int64_t len = __ldg(a.lens + b);
+    if (threadIdx.x == 0 && (len < 0 || len > static_cast<int64_t>(a.max_pages) * a.page))
+      atomicOr(&g_attn_decode_error_flags, 2u);
+    if (clamp_len(a, b) == 0) {
+      const int n = a.kv_heads * a.group * D;
+      for (int i = 4 * threadIdx.x; i < n; i += 4 * kConsumers)
+        store4(a.out, b * a.out_stride + i, a.dtype, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+  }
+
+  bool dead = false;
+  int g = 0;
+  while (w.left > 0) {
+    // ------------------------- one unit (or a part of it) -------------------------
+    const int b = w.b, hk = w.unit / a.chunks, chunk = w.unit - hk * a.chunks;
+    const int unit_n = w.n, tile0 = w.tile, unit = w.unit;
+    const int hc = min(C::kHeads, a.group - chunk * C::kHeads);      // heads of this chunk
+    const int h0 = hk * a.group + chunk * C::kHeads;
+    const int64_t len = clamp_len(a, b);
+    uint32_t qh[D / 8], ql[D / 8];
+    float factor[kH];
+    factor[0] = query_row<D, R == kSplit>(a, b * a.q_stride + static_cast<int64_t>(h0 + gq) * D, gq < hc, j, qh, ql);
+    if (R == kTwo) {
+      uint32_t none[D / 8];
+      factor[kH - 1] = query_row<D, false>(a, b * a.q_stride + static_cast<int64_t>(h0 + gq + 8) * D, gq + 8 < hc, j, ql, none);
+    }
+
+    float o[D / 8][4], m[kH], l[kH];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+#pragma unroll
+    for (int h = 0; h < kH; ++h) m[h] = -INFINITY, l[h] = 0.0f;
+
+    int n_here = static_cast<int>(min(static_cast<int64_t>(unit_n - tile0), w.left));
+    for (int t = tile0; t < tile0 + n_here; ++t, ++g) {
+      const int s = g % C::kStages;
+      if (!dead && !warp_wait(full(s), (g / C::kStages) & 1)) {
+        fail();
+        dead = true;
+      }
+      const int valid = static_cast<int>(min(static_cast<int64_t>(kTile), len - static_cast<int64_t>(t) * kTile)) - 16 * warp;
+      if (!dead && valid > 0) {
+        const uint32_t kb = base + s * C::kCodes, vb = kb + C::kOffV;
+        const uint32_t ksb = base + C::kOffKs + s * C::kScales + 16 * warp * 2 * C::kBlocks;
+        const uint32_t vsb = ksb + (C::kOffVs - C::kOffKs);
+        // ---- scores of the lane's tokens ta, tb, 8 + ta, 8 + tb
+        float p[kH][4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float da[C::kBlocks], db[C::kBlocks];
+          if constexpr (D == 128) {
+            const uint2 u = lds64(ksb + (8 * x + ta) * 8), v = lds64(ksb + (8 * x + tb) * 8);
+            const float2 u0 = __half22float2(dev::bits_h2(u.x)), u1 = __half22float2(dev::bits_h2(u.y));
+            const float2 v0 = __half22float2(dev::bits_h2(v.x)), v1 = __half22float2(dev::bits_h2(v.y));
+            da[0] = u0.x, da[1] = u0.y, da[2] = u1.x, da[3] = u1.y;
+            db[0] = v0.x, db[1] = v0.y, db[2] = v1.x, db[3] = v1.y;
+          } else {
+            const float2 u = __half22float2(dev::bits_h2(lds32(ksb + (8 * x + ta) * 4)));
+            const float2 v = __half22float2(dev::bits_h2(lds32(ksb + (8 * x + tb) * 4)));
+            da[0] = u.x, da[1] = u.y, db[0] = v.x, db[1] = v.y;
+          }
+          float sa[kH] = {}, sb[kH] = {};
+#pragma unroll
+          for (int bl = 0; bl < C::kBlocks; ++bl) {
+            const uint2 c8 = lds64(kb + 8 * x * D + (off_k ^ (32u * bl)));
+            uint32_t b0, b1, b2, b3;
+            codes_to_h2(c8.x, b0, b1);
+            codes_to_h2(c8.y, b2, b3);
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t z = 0;
+            mma_f16(acc, qh[4 * bl], R == kOne ? z : ql[4 * bl], qh[4 * bl + 1], R == kOne ? z : ql[4 * bl + 1], b0, b1);
+            mma_f16(acc, qh[4 * bl + 2], R == kOne ? z : ql[4 * bl + 2], qh[4 * bl + 3], R == kOne ? z : ql[4 * bl + 3], b2, b3);
+            if (R == kSplit) acc[0] += acc[2], acc[1] += acc[3];
+            sa[0] = fmaf(da[bl], acc[0], sa[0]);
+            sb[0] = fmaf(db[bl], acc[1], sb[0]);
+            if (R == kTwo) {
+              sa[kH - 1] = fmaf(da[bl], acc[2], sa[kH - 1]);
+              sb[kH - 1] = fmaf(db[bl], acc[3], sb[kH - 1]);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            p[h][2 * x] = 8 * x + ta < valid ? sa[h] * factor[h] : -INFINITY;
+            p[h][2 * x + 1] = 8 * x + tb < valid ? sb[h] * factor[h] : -INFINITY;
+          }
+        }
+        // ---- running maximum (shared by the four lanes of a head) and sum
+        float top[kH];
+        bool grow = false;
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+          top[h] = fmaxf(fmaxf(p[h][0], p[h][1]), fmaxf(p[h][2], p[h][3]));
+          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+          grow |= top[h] > m[h] + kLazy;
+        }
+        // The maximum is only a reference point: it may lag while no exponent
+        // passes 2^8, which spares most of the rescaling.
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            const float mn = fmaxf(m[h], top[h]);
+            const float c = m[h] == mn ? 1.0f : exp2_approx(m[h] - mn);
+            m[h] = mn;
+            l[h] *= c;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              if (R != kTwo) {
+                o[i][0] *= c, o[i][1] *= c;
+                if (R == kSplit) o[i][2] *= c, o[i][3] *= c;
+              } else {
+                o[i][2 * h] *= c, o[i][2 * h + 1] *= c;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[h][i] = exp2_approx(p[h][i] - m[h]);
+            l[h] += p[h][i];
+          }
+        }
+        // ---- values: one block of 32 at a time
+        uint2 sc[4];     // the tokens' value scales
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = (i >> 1) * 8 + (i & 1 ? tb : ta);
+          sc[i] = D == 128 ? lds64(vsb + tok * 8) : make_uint2(lds32(vsb + tok * 4), 0u);
+          if (tok >= valid) sc[i] = make_uint2(0u, 0u);      // whatever lies behind the last token
+        }
+#pragma unroll
+        for (int bl = 0; bl < C::kBlocks; ++bl) {
+          uint32_t hi[kH][4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 d2 = __half22float2(dev::bits_h2(bl < 2 ? sc[i].x : sc[i].y));
+            const float d = (bl & 1) ? d2.y : d2.x;
+#pragma unroll
+            for (int h = 0; h < kH; ++h) {
+              const float x = p[h][i] * d;
+              if (R == kSplit) {
+                hi[h][i] = __float_as_uint(x) & 0xFFFFE000u;              // tf32, exactly
+                lo[i] = __float_as_uint(x - __uint_as_float(hi[h][i]));
+              } else {
+                hi[h][i] = __float_as_uint(x) + 0x1000u;                  // to nearest: the MMA drops 13 bits
+              }
+            }
+          }
+          const uint32_t x32 = 32u * bl;
+          uint32_t va0[4], vb0[4], va1[4], vb1[4];
+          codes_to_f32(lds32(vb + (off_va ^ x32)), va0);
+          codes_to_f32(lds32(vb + (off_vb ^ x32)), vb0);
+          codes_to_f32(lds32(vb + 8 * D + (off_va ^ x32)), va1);
+          codes_to_f32(lds32(vb + 8 * D + (off_vb ^ x32)), vb1);
+          const uint32_t z = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float(&acc)[4] = o[4 * bl + i];
+            const uint32_t r0 = R == kOne ? z : R == kSplit ? lo[0] : hi[kH - 1][0];
+            const uint32_t r1 = R == kOne ? z : R == kSplit ? lo[1] : hi[kH - 1][1];
+            const uint32_t r2 = R == kOne ? z : R == kSplit ? lo[2] : hi[kH - 1][2];
+            const uint32_t r3 = R == kOne ? z : R == kSplit ? lo[3] : hi[kH - 1][3];
+            mma_tf32(acc, hi[0][0], r0, hi[0][1], r1, va0[i], vb0[i]);
+            mma_tf32(acc, hi[0][2], r2, hi[0][3], r3, va1[i], vb1[i]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(empty(s));
+    }
+
+    // ------------------ the four warps' parts of the unit, joined ------------------
+    // Lane (gq, j) holds dims 32 bl + 8 j .. + 7 of its heads.
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if (j == 0) {
+        ml[2 * (warp * C::kHeads + gq + 8 * h)] = m[h];
+        ml[2 * (warp * C::kHeads + gq + 8 * h) + 1] = l[h];
+      }
+#pragma unroll
+      for (int bl = 0; bl < C::kBlocks; ++bl) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float(&acc)[4] = o[4 * bl + i];
+          v[i] = R == kSplit ? acc[0] + acc[2] : acc[2 * h];
+          v[4 + i] = R == kSplit ? acc[1] + acc[3] : acc[2 * h + 1];
+        }
+        float4* to = reinterpret_cast<float4*>(red + (warp * C::kHeads + gq + 8 * h) * C::kRedStride + 32 * bl + 8 * j);
+        to[0] = make_float4(v[0], v[1], v[2], v[3]);
+        to[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    }
+    consumer_sync();
+    const bool whole = n_here == unit_n;
+    const int slot = 2 * cta + (unit_start >= first ? 1 : 0);
+    constexpr int kVecs = D / 4;
+    // whole units: the result; parts: o, m and l
+    auto join4 = [&](bool finish, float* part) {
+      for (int i = threadIdx.x; i < hc * kVecs; i += kConsumers) {
+        const int h = i / kVecs, d4 = i - h * kVecs;
+        float top = -INFINITY, L = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) top = fmaxf(top, ml[2 * (x * C::kHeads + h)]);
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) {
+          const float mx = ml[2 * (x * C::kHeads + h)];
+          const float c = mx == -INFINITY ? 0.0f : exp2_approx(mx - top);
+          L = fmaf(c, ml[2 * (x * C::kHeads + h) + 1], L);
+          const float4 v = *reinterpret_cast<const float4*>(red + (x * C::kHeads + h) * C::kRedStride + 4 * d4);
+          O.x = fmaf(c, v.x, O.x), O.y = fmaf(c, v.y, O.y), O.z = fmaf(c, v.z, O.z), O.w = fmaf(c, v.w, O.w);
+        }
+        if (finish) {
+          const float inv = __fdividef(1.0f, L);
+          store4(a.out, b * a.out_stride + static_cast<int64_t>(h0 + h) * D + 4 * d4, a.dtype,
+                 make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
+        } else {
+          float* to = part + h * C::kRedStride;
+          __stcg(reinterpret_cast<float4*>(to + 4 * d4), O);
+          if (d4 == 0) __stcg(reinterpret_cast<float2*>(to + D), make_float2(top, L));
+        }
+      }
+    };
+    const int64_t part_floats = static_cast<int64_t>(a.rows) * C::kRedStride;
+    join4(whole, a.part + slot * part_floats);
+    if (!whole) {
+      // the CTA that arrives last adds up the unit's parts, in tile order
+      const int64_t unit_first = unit_start;
+      const int c0 = split.owner(unit_first), c1 = split.owner(unit_first + unit_n - 1);
+      __threadfence();
+      consumer_sync();
+      int* counter = a.counters + static_cast<int64_t>(b) * U + unit;
+      if (threadIdx.x == 0) {
+        const int old = atomicAdd(counter, 1);
+        __threadfence();
+        *last_flag = old == c1 - c0;
+        if (old == c1 - c0) *counter = 0;
+      }
+      consumer_sync();
+      if (*last_flag) {
+        auto part_of = [&](int c) {
+          return a.part + (2 * static_cast<int64_t>(c) + (unit_first >= split.start(c) ? 1 : 0)) * part_floats;
+        };
+        // maximum of each head over the parts, then each warp adds a quarter of them
+        for (int h = warp; h < hc; h += kWarps) {
+          float top = -INFINITY;
+          for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, __ldcg(part_of(c) + h * C::kRedStride + D));
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+          if (lane == 0) top_s[h] = top;
+        }
+        consumer_sync();
+        for (int i = lane; i < hc * kVecs; i += 32) {
+          const int h = i / kVecs, d4 = i - h * kVecs;
+          const float top = top_s[h];
+          float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+          float L = 0.0f;
+#pragma unroll 4
+          for (int c = c0 + warp; c <= c1; c += kWarps) {
+            const float* from = part_of(c) + h * C::kRedStride;
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(from + D));
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(from + 4 * d4));
+            const float f = exp2_approx(x.x - top);
+            L = fmaf(f, x.y, L);
+            O.x = fmaf(f, v.x, O.x), O.y = fmaf(f, v.y, O.y), O.z = fmaf(f, v.z, O.z), O.w = fmaf(f, v.w, O.w);
+          }
+          *reinterpret_cast<float4*>(red + (warp * C::kHeads + h) * C::kRedStride + 4 * d4) = O;
+          if (d4 == 0) {
+            ml[2 * (warp * C::kHeads + h)] = top;
+            ml[2 * (warp * C::kHeads + h) + 1] = L;
+          }
+        }
+        consumer_sync();
+        join4(true, nullptr);
+      }
+    }
+    consumer_sync();      // red and ml are written again by the next unit
+    // on to the next unit
+    w.left -= n_here;
+    if (w.left > 0) {
+      unit_start += unit_n;
+      w.tile = 0;
+      if (++w.unit == U) {
+        w.unit = 0;
+        next_sequence(a, w);
+      }
+    }
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// The codes as [all rows][D] bytes, boxes of `gran` rows.
+bool code_map(CUtensorMap* map, int8_t* codes, const nvq_kv_cache& c, int gran) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.head_dim),
+                              static_cast<cuuint64_t>(c.n_pages * c.n_kv_heads * c.page_size)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.head_dim)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(c.head_dim), static_cast<cuuint32_t>(gran)};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE,
+                c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, Rows R>
+cudaError_t decode_launch(const nvq_kv_cache& c, DecodeArgs a, cudaStream_t stream) {
+  using C = Cfg<D, R>;
+  CUtensorMap k_map, v_map;
+  const int gran = c.page_size % kTile == 0 ? kTile : 16;
+  if (!code_map(&k_map, c.k_codes, c, gran) || !code_map(&v_map, c.v_codes, c, gran))
+    return cudaErrorInvalidValue;
+  static SmemAttrOnce attr;
+  cudaError_t e = attr.ensure(attn_decode_kernel<D, R>, C::kSmem);
+  if (e != cudaSuccess) return e;
+  a.chunks = (a.group + C::kHeads - 1) / C::kHeads;
+  a.rows = std::min(a.group, C::kHeads);
+  // no more CTAs than the tables can hold tiles
+  const int64_t cap = (static_cast<int64_t>(a.max_pages) * a.page + kTile - 1) / kTile;
+  const int64_t tiles = std::max<int64_t>(1, a.B * cap) * a.kv_heads * a.chunks;
+  const int64_t grid = std::min<int64_t>(static_cast<int64_t>(device_sm_count()) * C::kCtas, tiles);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute pdl;
+  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, R>, k_map, v_map, a);
 }
 
 }  // namespace
 
+// Two parts per CTA, up to 16 rows of head_dim + 4 floats.
 size_t attn_decode_workspace_size(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim) {
-  return 16;
+  const int64_t rows = std::min<int64_t>(16, heads / kv_heads);
+  return static_cast<size_t>(device_sm_count()) * 3 * 2 * rows * (head_dim + 4) * sizeof(float);
 }
 
 cudaError_t launch_attn_decode(const nvq_kv_cache& c, const int32_t* seq_lens,
@@ -106,16 +788,33 @@ cudaError_t launch_attn_decode(const nvq_kv_cache& c, const int32_t* seq_lens,
                                const void* q, int64_t q_stride, int64_t heads, float scale,
                                int dtype, void* out, int64_t out_stride, int32_t* counters,
                                void* workspace, cudaStream_t stream) {
-  const DecodeArgs a = {c.k_codes, reinterpret_cast<const __half*>(c.k_scales), c.v_codes,
-                        reinterpret_cast<const __half*>(c.v_scales), seq_lens, block_table,
-                        static_cast<int>(max_pages), static_cast<int>(c.n_pages),
-                        static_cast<int>(c.page_size), static_cast<int>(c.n_kv_heads),
-                        static_cast<int>(heads), scale * 1.4426950408889634f};
-  switch (dtype) {
-    case NVQ_F32: return decode_t<float>(c, a, B, q, q_stride, out, out_stride, stream);
-    case NVQ_F16: return decode_t<__half>(c, a, B, q, q_stride, out, out_stride, stream);
-    default: return decode_t<__nv_bfloat16>(c, a, B, q, q_stride, out, out_stride, stream);
-  }
+  DecodeArgs a = {};
+  a.ks = reinterpret_cast<const __half*>(c.k_scales);
+  a.vs = reinterpret_cast<const __half*>(c.v_scales);
+  a.lens = seq_lens;
+  a.table = block_table;
+  a.q = q;
+  a.out = out;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.counters = counters;
+  a.part = static_cast<float*>(workspace);
+  a.B = static_cast<int>(B);
+  a.max_pages = static_cast<int>(max_pages);
+  a.n_pages = static_cast<int>(c.n_pages);
+  a.page = static_cast<int>(c.page_size);
+  a.kv_heads = static_cast<int>(c.n_kv_heads);
+  a.group = static_cast<int>(heads / c.n_kv_heads);
+  a.dtype = dtype;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  const Rows r = dtype == NVQ_F32 ? kSplit : a.group <= 8 ? kOne : kTwo;
+  if (c.head_dim == 64)
+    return r == kSplit ? decode_launch<64, kSplit>(c, a, stream)
+           : r == kOne ? decode_launch<64, kOne>(c, a, stream)
+                       : decode_launch<64, kTwo>(c, a, stream);
+  return r == kSplit ? decode_launch<128, kSplit>(c, a, stream)
+         : r == kOne ? decode_launch<128, kOne>(c, a, stream)
+                     : decode_launch<128, kTwo>(c, a, stream);
 }
 
 cudaError_t attn_decode_error_flags(bool clear, unsigned int* flags) {
