@@ -16,22 +16,26 @@
 // arrives last at the unit's counter joins them in the order of the tiles
 // (the result does not depend on timing) and sets the counter back to 0.
 //
-// Copies.  One producer warp moves tiles to shared memory: codes by 2-D TMA
-// (64 rows, or four boxes of 16 where pages end inside a tile), swizzled so
-// that both read patterns below are free of bank conflicts; scales by 1-D bulk
-// copies.  Four consumer warps take 16 tokens of each tile.
+// Copies.  Tiles go to a ring in shared memory: codes by 2-D TMA (64 rows, or
+// four boxes of 16 where pages end inside a tile), swizzled so that both read
+// patterns below are free of bank conflicts; scales by 1-D bulk copies.  Four
+// warps take 16 tokens of each tile.  Warp 0 issues the copies as well: a
+// producer warp of its own would cost each of three CTAs per SM a quarter of
+// its registers, and the accumulators need them.
 //
 // Scores (m16n8k16, fp16 operands): A holds the queries, B the codes of 8
-// tokens, which are exact in fp16.  Each query row is scaled by a power of
+// tokens, which are exact in
+// fp16 (as code + 128, the bias coming off in fp32).  Each query row is scaled by a power of
 // two to just below 2^14 before it is rounded, so 16-bit queries are exact
 // and fp32 ones become an exact pair hi + lo of at least 22 bits, in rows g and
 // g + 8 of the same fragment.  Two MMAs cover one block of 32 values; its
 // scale is then applied in fp32.
 //
-// Values (m16n8k8, tf32 operands): the accumulators of the scores are, in the
-// same lanes, the left operand of this product.  A = p_j * scale_j of one
-// 32-block, in tf32 because the scales need fp32's range (fp32 rows: hi + lo
-// again), B = the codes, exact.
+// Values (m16n8k8, tf32 operands), transposed, o^T = V^T p^T: A holds 16 dims of
+// 8 tokens, exact, B = p_j * scale_j of 8 heads, in tf32 because the scales
+// need fp32's range (fp32 rows: hi, then lo).  The accumulators of the
+// scores are, in the same lanes, this B; and with 8 heads the sums take half
+// the registers that heads as rows of 16 would.
 //
 // These are warp-level MMAs: there are at most 16 query rows per key-value
 // head, an eighth of the smallest tcgen05 tile, and the operands change
@@ -52,9 +56,8 @@ namespace nvq {
 namespace {
 
 constexpr int kTile = 64;            // tokens of a tile
-constexpr int kWarps = 4;            // consumer warps, 16 tokens of a tile each
-constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kConsumers = 32 * kWarps;
+constexpr int kWarps = 4;            // 16 tokens of a tile each
+constexpr int kThreads = 32 * kWarps;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr float kLazy = 8.0f;        // the running maximum may lag by this power of two
 
@@ -82,15 +85,14 @@ template <int D, Rows R>
 struct Cfg {
   static constexpr int kHeads = R == kTwo ? 16 : 8;          // heads of a chunk
   static constexpr int kBlocks = D / 32;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = 4;
   static constexpr int kCodes = kTile * D;                   // bytes of a tile's codes
   static constexpr int kScales = kTile * kBlocks * 2;
-  static constexpr int kRedStride = D + 4;                   // float4 stores of 8 rows hit all banks
+  static constexpr int kPart = D + 4;                        // floats of a part's row: o, m, l
   static constexpr int kOffV = kStages * kCodes;
   static constexpr int kOffKs = 2 * kStages * kCodes;
   static constexpr int kOffVs = kOffKs + kStages * kScales;
-  static constexpr int kOffRed = kOffVs + kStages * kScales;
-  static constexpr int kOffMl = kOffRed + kWarps * kHeads * kRedStride * 4;
+  static constexpr int kOffMl = kOffVs + kStages * kScales;
   static constexpr int kOffBars = kOffMl + kWarps * kHeads * 8 + kHeads * 4;
   static constexpr int kSmem = kOffBars + 2 * kStages * 8 + 16 + 1024;
   static constexpr int kCtas = R == kTwo ? 2 : 3;            // per SM
@@ -113,7 +115,6 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b) {
 // Split of W tiles over G CTAs: the first W % G have one more.
 struct Split {
   int64_t base, rem;
-  __device__ Split(int64_t W, int G) : base(W / G), rem(W % G) {}
   __device__ int64_t start(int64_t c) const { return c * base + (c < rem ? c : rem); }
   __device__ int owner(int64_t t) const {
     const int64_t big = rem * (base + 1);
@@ -181,19 +182,24 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   return v;
 }
 
-// Four int8 codes (u = code + 128 per byte) as exact fp16: 0x64bb is 1024 + u.
+// Four int8 codes as fp16 (u = code + 128 per byte): 0x00bb is u * 2^-24, the
+// subnormals and the first binade being evenly spaced, and tensor cores
+// take them exactly.  The bias comes off through the accumulator's start.
 __device__ __forceinline__ void codes_to_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
   const uint32_t u = w ^ 0x80808080u;
-  const __half2 bias = __half2half2(__ushort_as_half(0x6480));   // 1152
-  lo = dev::h2_bits(__hsub2(dev::bits_h2(__byte_perm(u, 0x64646464u, 0x4140)), bias));
-  hi = dev::h2_bits(__hsub2(dev::bits_h2(__byte_perm(u, 0x64646464u, 0x4342)), bias));
+  lo = __byte_perm(u, 0u, 0x4140);
+  hi = __byte_perm(u, 0u, 0x4342);
 }
-// The same as fp32: 0x4B0000bb is 2^23 + u.  The sums are exact.
+// The same as fp32: 0x4B0000bb is 2^23 + u.  The differences are exact.
 __device__ __forceinline__ void codes_to_f32(uint32_t w, uint32_t (&f)[4]) {
   const uint32_t u = w ^ 0x80808080u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    f[i] = __float_as_uint(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + i)) - 8388736.0f);
+  for (int i = 0; i < 4; i += 2)
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=r"(f[i]), "=r"(f[i + 1])
+        : "r"(__byte_perm(u, 0x4B000000u, 0x7440 + i)), "r"(__byte_perm(u, 0x4B000000u, 0x7441 + i)),
+          "r"(0xCB000080u));    // -(2^23 + 128)
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -236,17 +242,15 @@ __device__ __forceinline__ void store4(void* p, int64_t at, int dtype, float4 v)
   }
 }
 
-__device__ __forceinline__ void consumer_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
-}
-
 // One query row's values of this lane (8 per block: 32 * block + 8 * j ..) as
 // A fragments: scaled by a power of two so that the row's largest lies in
 // [2^13, 2^14), then rounded to fp16, and the remainder for `lo`.  Returns
-// the factor that turns the MMA's sums into powers of two.
+// the factor that turns the MMA's sums into powers of two; `start` is what the
+// sums over each block begin with, -128 * 2^-24 * sum of the operands.
 template <int D, bool LO>
 __device__ __forceinline__ float query_row(const DecodeArgs& a, int64_t at, bool on, int j,
-                                           uint32_t (&hi)[D / 8], uint32_t (&lo)[D / 8]) {
+                                           uint32_t (&hi)[D / 8], uint32_t (&lo)[D / 8],
+                                           float (&start)[D / 32], float (&start_lo)[D / 32]) {
   float x[D / 4], top = 0.0f;
 #pragma unroll
   for (int bl = 0; bl < D / 32; ++bl) {
@@ -264,16 +268,34 @@ __device__ __forceinline__ float query_row(const DecodeArgs& a, int64_t at, bool
   const int k = min(126, 140 - static_cast<int>(__float_as_uint(top) >> 23));
   const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    const float u = x[2 * i] * up, v = x[2 * i + 1] * up;
-    const __half2 h = __floats2half2_rn(u, v);
-    hi[i] = dev::h2_bits(h);
-    if (LO) {
+  for (int bl = 0; bl < D / 32; ++bl) {
+    start[bl] = 0.0f;
+    if (LO) start_lo[bl] = 0.0f;
+#pragma unroll
+    for (int i = 4 * bl; i < 4 * bl + 4; ++i) {
+      const float u = x[2 * i] * up, v = x[2 * i + 1] * up;
+      const __half2 h = __floats2half2_rn(u, v);
       const float2 f = __half22float2(h);
-      lo[i] = dev::h2_bits(__floats2half2_rn(u - f.x, v - f.y));
+      hi[i] = dev::h2_bits(h);
+      start[bl] += f.x + f.y;
+      if (LO) {
+        const __half2 r = __floats2half2_rn(u - f.x, v - f.y);
+        const float2 rf = __half22float2(r);
+        lo[i] = dev::h2_bits(r);
+        start_lo[bl] += rf.x + rf.y;
+      }
+    }
+    start[bl] += __shfl_xor_sync(0xffffffffu, start[bl], 1);
+    start[bl] += __shfl_xor_sync(0xffffffffu, start[bl], 2);
+    start[bl] *= -0x1p-17f;
+    if (LO) {
+      start_lo[bl] += __shfl_xor_sync(0xffffffffu, start_lo[bl], 1);
+      start_lo[bl] += __shfl_xor_sync(0xffffffffu, start_lo[bl], 2);
+      start_lo[bl] *= -0x1p-17f;
     }
   }
-  return a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  // 2^24 (the codes' unit) and 2^-k; k > -128 + 24 even for infinities
+  return a.scale_log2 * 0x1p24f * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
 }
 
 template <int D, Rows R>
@@ -307,6 +329,10 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
+  // what only the walk and the ends of units need stays out of the registers
+  // of the main loop
+  __shared__ Split split_s;
+  __shared__ Walk pw_s;          // the copies' position (warp 0)
   const int U = a.kv_heads * a.chunks;
   const int G = gridDim.x, cta = blockIdx.x;
   // every warp finds the CTA's first tile for itself (no hand-over): the sum
@@ -314,10 +340,10 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
   int64_t total = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) total += b0 + lane < a.B ? tiles_of(a, b0 + lane) : 0;
   total = warp_sum64(total) * U;
-  const Split split(total, G);
+  const Split split = {total / G, total % G};
   const int64_t first = split.start(cta);
   Walk w = {0, 0, 0, 1, split.start(cta + 1) - first};
-  int64_t unit_start = 0;       // tile number at which the unit of `w` starts
+  int64_t unit_start = 0;       // the first tile of the unit of `w`, counted from the CTA's first
   if (w.left > 0) {
     int64_t before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
@@ -336,7 +362,11 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
     const int64_t r = first - before * U;
     w.unit = static_cast<int>(r / w.n);
     w.tile = static_cast<int>(r - static_cast<int64_t>(w.unit) * w.n);
-    unit_start = first - w.tile;
+    unit_start = -w.tile;
+  }
+  if (threadIdx.x == 0) {
+    split_s = split;
+    pw_s = w;
   }
 
   auto fail = [&]() {
@@ -349,58 +379,87 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
     return __all_sync(0xffffffffu, got);
   };
 
-  if (warp == kWarps) {
-    // ------------------------------ producer --------------------------------
-    // Lane 4 * i + x copies granule i of array x (codes of K, of V, scales of
-    // K, of V): the whole tile where pages hold whole tiles, else 16 tokens.
-    const int gran = a.page % kTile == 0 ? kTile : 16;
+  // ------------------------------- the copies -------------------------------
+  // Warp 0 issues them beside its share of the work, so they are kept short:
+  // lane 4 * i + x copies granule i of array x (codes of K, of V, scales of K,
+  // of V): the whole tile where pages hold whole tiles, else 16 tokens.  Its
+  // place in the table moves on by a tile at a time, and the page is read
+  // one tile ahead of its copies.
+  const int gran_shift = a.page % kTile == 0 ? 6 : 4;
+  const int step_page = kTile / a.page, step_off = kTile % a.page;
+  int pg = 0;                   // tiles issued
+  int p_left = 0;               // tiles of the unit not issued yet (0: none is left at all)
+  int p_rem = 0;                // tokens from the next tile on
+  int p_idx = 0, p_off = 0;     // this lane's granule: column of the table, token in the page
+  int p_page = 0;
+  const int32_t* p_table = nullptr;
+  auto read_page = [&]() {
+    if (((lane >> 2) << gran_shift) < min(p_rem, kTile)) p_page = __ldg(p_table + p_idx);
+  };
+  auto begin_unit = [&]() {     // from pw_s, at some tile of a unit
+    const Walk pw = pw_s;
+    p_left = static_cast<int>(min(static_cast<int64_t>(pw.n - pw.tile), pw.left));
+    if (p_left <= 0) return;
+    const int64_t pos0 = static_cast<int64_t>(pw.tile) * kTile;
+    const int pos = static_cast<int>(pos0) + ((lane >> 2) << gran_shift);
+    p_rem = static_cast<int>(clamp_len(a, pw.b) - pos0);
+    p_idx = pos / a.page;
+    p_off = pos % a.page;
+    p_table = a.table + static_cast<int64_t>(pw.b) * a.max_pages;
+    read_page();
+  };
+  auto issue = [&]() {
+    if (p_left == 0) return;
+    const int s = pg % C::kStages;
+    if (!warp_wait(empty(s), ((pg / C::kStages) & 1) ^ 1)) {
+      fail();
+      p_left = 0;
+      return;
+    }
+    const int n = (min(p_rem, kTile) + (1 << gran_shift) - 1) >> gran_shift;    // granules with tokens
+    if (lane == 0) ptx::mbar_arrive_expect_tx(full(s), (n << gran_shift) * (2 * D + 4 * C::kBlocks));
+    __syncwarp();
     const int gi = lane >> 2, arr = lane & 3;
-    int g = 0;
-    bool more = w.left > 0;
-    for (; more; ++g) {
-      const int64_t len = clamp_len(a, w.b);
-      const int valid = static_cast<int>(min(static_cast<int64_t>(kTile), len - static_cast<int64_t>(w.tile) * kTile));
-      const int n = (valid + gran - 1) / gran;        // granules with tokens in them
-      const bool mine = gi < n;
-      int64_t row = 0;
-      if (mine) {
-        const int64_t pos = static_cast<int64_t>(w.tile) * kTile + gi * gran;
-        int page = __ldg(a.table + static_cast<int64_t>(w.b) * a.max_pages + pos / a.page);
-        if (page < 0 || page >= a.n_pages) {
-          atomicOr(&g_attn_decode_error_flags, 2u);
-          page = 0;
-        }
-        row = (static_cast<int64_t>(page) * a.kv_heads + w.unit / a.chunks) * a.page + pos % a.page;
+    if (gi < n) {
+      if (p_page < 0 || p_page >= a.n_pages) {
+        atomicOr(&g_attn_decode_error_flags, 2u);
+        p_page = 0;
       }
-      const int s = g % C::kStages;
-      if (!warp_wait(empty(s), ((g / C::kStages) & 1) ^ 1)) {
-        fail();
-        break;
-      }
-      if (lane == 0) ptx::mbar_arrive_expect_tx(full(s), n * gran * (2 * D + 4 * C::kBlocks));
-      __syncwarp();
-      if (mine) {
-        const uint32_t to = base + s * C::kCodes + gi * gran * D;
-        const uint32_t to_s = base + s * C::kScales + gi * gran * 2 * C::kBlocks;
-        if (arr == 0)
-          ptx::tma_load_2d(to, &k_map, 0, static_cast<int>(row), full(s));
-        else if (arr == 1)
-          ptx::tma_load_2d(to + C::kOffV, &v_map, 0, static_cast<int>(row), full(s));
-        else if (arr == 2)
-          ptx::bulk_load(to_s + C::kOffKs, a.ks + row * C::kBlocks, gran * 2 * C::kBlocks, full(s));
-        else
-          ptx::bulk_load(to_s + C::kOffVs, a.vs + row * C::kBlocks, gran * 2 * C::kBlocks, full(s));
-      }
-      __syncwarp();
-      advance(a, w, U);
-      more = w.left > 0;
+      const int row = (p_page * a.kv_heads + pw_s.unit / a.chunks) * a.page + p_off;
+      const int tok = gi << gran_shift;
+      if (arr < 2)
+        ptx::tma_load_2d(base + s * C::kCodes + tok * D + arr * C::kOffV, arr == 0 ? &k_map : &v_map, 0, row, full(s));
+      else
+        ptx::bulk_load(base + s * C::kScales + tok * 2 * C::kBlocks + (arr == 2 ? C::kOffKs : C::kOffVs),
+                       (arr == 2 ? a.ks : a.vs) + static_cast<int64_t>(row) * C::kBlocks,
+                       2 * C::kBlocks << gran_shift, full(s));
     }
-    if (*abort_flag) {
-      // the consumers may have stopped: wait for the copies in flight
-      for (int i = max(0, g - C::kStages); i < g; ++i)
-        ptx::mbar_wait_bounded(full(i % C::kStages), (i / C::kStages) & 1, nullptr, kWaitLimitNs);
+    ++pg;
+    if (--p_left > 0) {
+      p_rem -= kTile;
+      p_idx += step_page;
+      p_off += step_off;
+      if (p_off >= a.page) {
+        p_off -= a.page;
+        ++p_idx;
+      }
+      read_page();
+    } else {
+      Walk pw = pw_s;
+      const int here = static_cast<int>(min(static_cast<int64_t>(pw.n - pw.tile), pw.left));
+      pw.tile += here - 1;
+      pw.left -= here - 1;
+      advance(a, pw, U);
+      __syncwarp();
+      if (lane == 0) pw_s = pw;
+      __syncwarp();
+      begin_unit();
     }
-    return;
+  };
+  if (warp == 0) {
+    __syncwarp();
+    begin_unit();
+    for (int i = 0; i < C::kStages; ++i) issue();
   }
 
   // -------------------------------- consumers -------------------------------
@@ -417,7 +476,6 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
   const uint32_t off_vb = (16 * warp + tb) * D + (((gq >> 2) ^ swz(tb)) << 4) + (gq & 3) * 4;
   constexpr int kH = R == kTwo ? 2 : 1;      // heads of this lane: gq, and gq + 8
 
-  float* red = reinterpret_cast<float*>(smem + C::kOffRed);
   float* ml = reinterpret_cast<float*>(smem + C::kOffMl);            // [warp][head][m, l]
   float* top_s = ml + kWarps * C::kHeads * 2;                        // [head]
 
@@ -428,7 +486,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
       atomicOr(&g_attn_decode_error_flags, 2u);
     if (clamp_len(a, b) == 0) {
       const int n = a.kv_heads * a.group * D;
-      for (int i = 4 * threadIdx.x; i < n; i += 4 * kConsumers)
+      for (int i = 4 * threadIdx.x; i < n; i += 4 * kThreads)
         store4(a.out, b * a.out_stride + i, a.dtype, make_float4(0.f, 0.f, 0.f, 0.f));
     }
   }
@@ -441,29 +499,36 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
     const int unit_n = w.n, tile0 = w.tile, unit = w.unit;
     const int hc = min(C::kHeads, a.group - chunk * C::kHeads);      // heads of this chunk
     const int h0 = hk * a.group + chunk * C::kHeads;
-    const int64_t len = clamp_len(a, b);
+    // tokens from the first tile of this part on; only the last tile's matter
+    int rem = static_cast<int>(min(clamp_len(a, b) - static_cast<int64_t>(tile0) * kTile, int64_t{INT32_MAX}));
     uint32_t qh[D / 8], ql[D / 8];
     float factor[kH];
-    factor[0] = query_row<D, R == kSplit>(a, b * a.q_stride + static_cast<int64_t>(h0 + gq) * D, gq < hc, j, qh, ql);
+    float start[C::kBlocks], start2[C::kBlocks];       // of rows gq and gq + 8
+    factor[0] = query_row<D, R == kSplit>(a, b * a.q_stride + static_cast<int64_t>(h0 + gq) * D, gq < hc, j, qh, ql, start, start2);
     if (R == kTwo) {
       uint32_t none[D / 8];
-      factor[kH - 1] = query_row<D, false>(a, b * a.q_stride + static_cast<int64_t>(h0 + gq + 8) * D, gq + 8 < hc, j, ql, none);
+      float unused[C::kBlocks];
+      factor[kH - 1] = query_row<D, false>(a, b * a.q_stride + static_cast<int64_t>(h0 + gq + 8) * D, gq + 8 < hc, j, ql, none, start2, unused);
     }
 
-    float o[D / 8][4], m[kH], l[kH];
+    // o[n][2 * bl + x]: heads 8 n + 2 j (elements 0, 2) and 8 n + 2 j + 1 (1, 3),
+    // dims 32 bl + 4 gq + 2 x (0, 1) and the next one (2, 3)
+    float o[kH][D / 16][4], m[kH], l[kH];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    for (int n = 0; n < kH; ++n)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
 #pragma unroll
     for (int h = 0; h < kH; ++h) m[h] = -INFINITY, l[h] = 0.0f;
 
-    int n_here = static_cast<int>(min(static_cast<int64_t>(unit_n - tile0), w.left));
-    for (int t = tile0; t < tile0 + n_here; ++t, ++g) {
+    const int n_here = static_cast<int>(min(static_cast<int64_t>(unit_n - tile0), w.left));
+    for (int t = n_here; t > 0; --t, ++g, rem -= kTile) {
       const int s = g % C::kStages;
       if (!dead && !warp_wait(full(s), (g / C::kStages) & 1)) {
         fail();
         dead = true;
       }
-      const int valid = static_cast<int>(min(static_cast<int64_t>(kTile), len - static_cast<int64_t>(t) * kTile)) - 16 * warp;
+      const int valid = rem - 16 * warp;       // this warp's tokens (16 or more: all)
       if (!dead && valid > 0) {
         const uint32_t kb = base + s * C::kCodes, vb = kb + C::kOffV;
         const uint32_t ksb = base + C::kOffKs + s * C::kScales + 16 * warp * 2 * C::kBlocks;
@@ -491,7 +556,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
             uint32_t b0, b1, b2, b3;
             codes_to_h2(c8.x, b0, b1);
             codes_to_h2(c8.y, b2, b3);
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            float acc[4] = {start[bl], start[bl], R == kOne ? 0.f : start2[bl], R == kOne ? 0.f : start2[bl]};
             const uint32_t z = 0;
             mma_f16(acc, qh[4 * bl], R == kOne ? z : ql[4 * bl], qh[4 * bl + 1], R == kOne ? z : ql[4 * bl + 1], b0, b1);
             mma_f16(acc, qh[4 * bl + 2], R == kOne ? z : ql[4 * bl + 2], qh[4 * bl + 3], R == kOne ? z : ql[4 * bl + 3], b2, b3);
@@ -509,34 +574,29 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
             p[h][2 * x + 1] = 8 * x + tb < valid ? sb[h] * factor[h] : -INFINITY;
           }
         }
-        // ---- running maximum (shared by the four lanes of a head) and sum
+        // ---- running maximum (the same in the four lanes of a head) and sum.
+        // The maximum is only a reference point: it may lag while no exponent
+        // passes 2^8, so most tiles need no more than this vote.
         float top[kH];
         bool grow = false;
 #pragma unroll
         for (int h = 0; h < kH; ++h) {
           top[h] = fmaxf(fmaxf(p[h][0], p[h][1]), fmaxf(p[h][2], p[h][3]));
-          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-          top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
           grow |= top[h] > m[h] + kLazy;
         }
-        // The maximum is only a reference point: it may lag while no exponent
-        // passes 2^8, which spares most of the rescaling.
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int h = 0; h < kH; ++h) {
+            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
             const float mn = fmaxf(m[h], top[h]);
             const float c = m[h] == mn ? 1.0f : exp2_approx(m[h] - mn);
             m[h] = mn;
             l[h] *= c;
+            // the factors of the heads whose sums this lane holds
+            const float c0 = __shfl_sync(0xffffffffu, c, 8 * j), c1 = __shfl_sync(0xffffffffu, c, 8 * j + 4);
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              if (R != kTwo) {
-                o[i][0] *= c, o[i][1] *= c;
-                if (R == kSplit) o[i][2] *= c, o[i][3] *= c;
-              } else {
-                o[i][2 * h] *= c, o[i][2 * h + 1] *= c;
-              }
-            }
+            for (int i = 0; i < D / 16; ++i) o[h][i][0] *= c0, o[h][i][1] *= c1, o[h][i][2] *= c0, o[h][i][3] *= c1;
           }
         }
 #pragma unroll
@@ -574,30 +634,71 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
             }
           }
           const uint32_t x32 = 32u * bl;
-          uint32_t va0[4], vb0[4], va1[4], vb1[4];
-          codes_to_f32(lds32(vb + (off_va ^ x32)), va0);
-          codes_to_f32(lds32(vb + (off_vb ^ x32)), vb0);
-          codes_to_f32(lds32(vb + 8 * D + (off_va ^ x32)), va1);
-          codes_to_f32(lds32(vb + 8 * D + (off_vb ^ x32)), vb1);
-          const uint32_t z = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float(&acc)[4] = o[4 * bl + i];
-            const uint32_t r0 = R == kOne ? z : R == kSplit ? lo[0] : hi[kH - 1][0];
-            const uint32_t r1 = R == kOne ? z : R == kSplit ? lo[1] : hi[kH - 1][1];
-            const uint32_t r2 = R == kOne ? z : R == kSplit ? lo[2] : hi[kH - 1][2];
-            const uint32_t r3 = R == kOne ? z : R == kSplit ? lo[3] : hi[kH - 1][3];
-            mma_tf32(acc, hi[0][0], r0, hi[0][1], r1, va0[i], vb0[i]);
-            mma_tf32(acc, hi[0][2], r2, hi[0][3], r3, va1[i], vb1[i]);
+          for (int x = 0; x < 2; ++x) {      // tokens 0-7, tokens 8-15
+            uint32_t va[4], vc[4];
+            codes_to_f32(lds32(vb + 8 * x * D + (off_va ^ x32)), va);
+            codes_to_f32(lds32(vb + 8 * x * D + (off_vb ^ x32)), vc);
+#pragma unroll
+            for (int n = 0; n < kH; ++n) {
+              mma_tf32(o[n][2 * bl], va[0], va[1], vc[0], vc[1], hi[n][2 * x], hi[n][2 * x + 1]);
+              mma_tf32(o[n][2 * bl + 1], va[2], va[3], vc[2], vc[3], hi[n][2 * x], hi[n][2 * x + 1]);
+            }
+            if (R == kSplit) {
+              mma_tf32(o[0][2 * bl], va[0], va[1], vc[0], vc[1], lo[2 * x], lo[2 * x + 1]);
+              mma_tf32(o[0][2 * bl + 1], va[2], va[3], vc[2], vc[3], lo[2 * x], lo[2 * x + 1]);
+            }
           }
         }
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(empty(s));
+      // refill the stage of the tile before this one: the other warps have
+      // most likely left it
+      if (warp == 0 && g > 0) issue();
     }
 
     // ------------------ the four warps' parts of the unit, joined ------------------
-    // Lane (gq, j) holds dims 32 bl + 8 j .. + 7 of its heads.
+    // Eight heads at a time, in the codes of the tile just used: its stage is
+    // filled again only after the next tile.  Row (warp, head) holds D floats,
+    // its float4s exchanged by the head so that the four heads that lanes j
+    // write fall on different banks.
+    const int s_last = (g - 1) % C::kStages;
+    auto red = [&](int x, int h, int d4) -> float4* {
+      unsigned char* at = smem + s_last * C::kCodes + (x >> 1) * C::kOffV;
+      return reinterpret_cast<float4*>(at) + (((x & 1) * 8 + h) * (D / 4) + (d4 ^ (((h >> 1) & 3) << 1)));
+    };
+    constexpr int kVecs = D / 4;
+    // Sum of the four warps' rows of heads 8 n + h; the result, or a part.
+    auto join4 = [&](int n, float* part) {
+      for (int i = threadIdx.x; i < min(8, hc - 8 * n) * kVecs; i += kThreads) {
+        const int h = i / kVecs, d4 = i - h * kVecs, hn = 8 * n + h;
+        float top = -INFINITY, L = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) top = fmaxf(top, ml[2 * (x * C::kHeads + hn)]);
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) {
+          const float mx = ml[2 * (x * C::kHeads + hn)];
+          const float c = mx == -INFINITY ? 0.0f : exp2_approx(mx - top);
+          L = fmaf(c, ml[2 * (x * C::kHeads + hn) + 1], L);
+          const float4 v = *red(x, h, d4);
+          O.x = fmaf(c, v.x, O.x), O.y = fmaf(c, v.y, O.y), O.z = fmaf(c, v.z, O.z), O.w = fmaf(c, v.w, O.w);
+        }
+        if (part == nullptr) {
+          const float inv = __fdividef(1.0f, L);
+          store4(a.out, b * a.out_stride + static_cast<int64_t>(h0 + hn) * D + 4 * d4, a.dtype,
+                 make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
+        } else {
+          float* to = part + hn * C::kPart;
+          __stcg(reinterpret_cast<float4*>(to + 4 * d4), O);
+          if (d4 == 0) __stcg(reinterpret_cast<float2*>(to + D), make_float2(top, L));
+        }
+      }
+    };
+    const bool whole = n_here == unit_n;
+    const int slot = 2 * cta + (unit_start >= 0 ? 1 : 0);
+    const int64_t part_floats = static_cast<int64_t>(a.rows) * C::kPart;
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
@@ -606,105 +707,77 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
         ml[2 * (warp * C::kHeads + gq + 8 * h)] = m[h];
         ml[2 * (warp * C::kHeads + gq + 8 * h) + 1] = l[h];
       }
+      __syncthreads();      // every warp has left the tile's codes, or the heads before
 #pragma unroll
       for (int bl = 0; bl < C::kBlocks; ++bl) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float(&acc)[4] = o[4 * bl + i];
-          v[i] = R == kSplit ? acc[0] + acc[2] : acc[2 * h];
-          v[4 + i] = R == kSplit ? acc[1] + acc[3] : acc[2 * h + 1];
-        }
-        float4* to = reinterpret_cast<float4*>(red + (warp * C::kHeads + gq + 8 * h) * C::kRedStride + 32 * bl + 8 * j);
-        to[0] = make_float4(v[0], v[1], v[2], v[3]);
-        to[1] = make_float4(v[4], v[5], v[6], v[7]);
+        const float(&u)[4] = o[h][2 * bl];
+        const float(&v)[4] = o[h][2 * bl + 1];
+        *red(warp, 2 * j, 8 * bl + gq) = make_float4(u[0], u[2], v[0], v[2]);
+        *red(warp, 2 * j + 1, 8 * bl + gq) = make_float4(u[1], u[3], v[1], v[3]);
       }
+      __syncthreads();
+      join4(h, whole ? nullptr : a.part + slot * part_floats);
     }
-    consumer_sync();
-    const bool whole = n_here == unit_n;
-    const int slot = 2 * cta + (unit_start >= first ? 1 : 0);
-    constexpr int kVecs = D / 4;
-    // whole units: the result; parts: o, m and l
-    auto join4 = [&](bool finish, float* part) {
-      for (int i = threadIdx.x; i < hc * kVecs; i += kConsumers) {
-        const int h = i / kVecs, d4 = i - h * kVecs;
-        float top = -INFINITY, L = 0.0f;
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x) top = fmaxf(top, ml[2 * (x * C::kHeads + h)]);
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x) {
-          const float mx = ml[2 * (x * C::kHeads + h)];
-          const float c = mx == -INFINITY ? 0.0f : exp2_approx(mx - top);
-          L = fmaf(c, ml[2 * (x * C::kHeads + h) + 1], L);
-          const float4 v = *reinterpret_cast<const float4*>(red + (x * C::kHeads + h) * C::kRedStride + 4 * d4);
-          O.x = fmaf(c, v.x, O.x), O.y = fmaf(c, v.y, O.y), O.z = fmaf(c, v.z, O.z), O.w = fmaf(c, v.w, O.w);
-        }
-        if (finish) {
-          const float inv = __fdividef(1.0f, L);
-          store4(a.out, b * a.out_stride + static_cast<int64_t>(h0 + h) * D + 4 * d4, a.dtype,
-                 make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
-        } else {
-          float* to = part + h * C::kRedStride;
-          __stcg(reinterpret_cast<float4*>(to + 4 * d4), O);
-          if (d4 == 0) __stcg(reinterpret_cast<float2*>(to + D), make_float2(top, L));
-        }
-      }
-    };
-    const int64_t part_floats = static_cast<int64_t>(a.rows) * C::kRedStride;
-    join4(whole, a.part + slot * part_floats);
     if (!whole) {
       // the CTA that arrives last adds up the unit's parts, in tile order
-      const int64_t unit_first = unit_start;
+      const Split split = split_s;
+      const int64_t unit_first = split.start(cta) + unit_start;
       const int c0 = split.owner(unit_first), c1 = split.owner(unit_first + unit_n - 1);
       __threadfence();
-      consumer_sync();
-      int* counter = a.counters + static_cast<int64_t>(b) * U + unit;
+      __syncthreads();
       if (threadIdx.x == 0) {
+        int* counter = a.counters + static_cast<int64_t>(b) * U + unit;
         const int old = atomicAdd(counter, 1);
         __threadfence();
         *last_flag = old == c1 - c0;
         if (old == c1 - c0) *counter = 0;
       }
-      consumer_sync();
+      __syncthreads();
       if (*last_flag) {
-        auto part_of = [&](int c) {
-          return a.part + (2 * static_cast<int64_t>(c) + (unit_first >= split.start(c) ? 1 : 0)) * part_floats;
-        };
+        // only the first part can lie in a CTA's second slot: the others
+        // start where their CTA does
+        const float* first_part = a.part + (2 * static_cast<int64_t>(c0) + (unit_first >= split.start(c0) ? 1 : 0)) * part_floats;
+        const float* next_parts = a.part + 2 * (static_cast<int64_t>(c0) + 1) * part_floats;
+        auto part_of = [&](int i) { return i == 0 ? first_part : next_parts + 2 * (i - 1) * part_floats; };
+        const int parts = c1 - c0 + 1;
         // maximum of each head over the parts, then each warp adds a quarter of them
         for (int h = warp; h < hc; h += kWarps) {
           float top = -INFINITY;
-          for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, __ldcg(part_of(c) + h * C::kRedStride + D));
+          for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldcg(part_of(i) + h * C::kPart + D));
 #pragma unroll
           for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
           if (lane == 0) top_s[h] = top;
         }
-        consumer_sync();
-        for (int i = lane; i < hc * kVecs; i += 32) {
-          const int h = i / kVecs, d4 = i - h * kVecs;
-          const float top = top_s[h];
-          float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-          float L = 0.0f;
-#pragma unroll 4
-          for (int c = c0 + warp; c <= c1; c += kWarps) {
-            const float* from = part_of(c) + h * C::kRedStride;
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(from + D));
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(from + 4 * d4));
-            const float f = exp2_approx(x.x - top);
-            L = fmaf(f, x.y, L);
-            O.x = fmaf(f, v.x, O.x), O.y = fmaf(f, v.y, O.y), O.z = fmaf(f, v.z, O.z), O.w = fmaf(f, v.w, O.w);
+        for (int n = 0; n < kH; ++n) {
+          __syncthreads();
+          for (int i = lane; i < min(8, hc - 8 * n) * kVecs; i += 32) {
+            const int h = i / kVecs, d4 = i - h * kVecs, hn = 8 * n + h;
+            const float top = top_s[hn];
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+            float L = 0.0f;
+#pragma unroll 8
+            for (int x = warp; x < parts; x += kWarps) {
+              const float* from = part_of(x) + hn * C::kPart;
+              const float2 y = __ldcg(reinterpret_cast<const float2*>(from + D));
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(from + 4 * d4));
+              const float f = exp2_approx(y.x - top);
+              L = fmaf(f, y.y, L);
+              O.x = fmaf(f, v.x, O.x), O.y = fmaf(f, v.y, O.y), O.z = fmaf(f, v.z, O.z), O.w = fmaf(f, v.w, O.w);
+            }
+            *red(warp, h, d4) = O;
+            if (d4 == 0) {
+              ml[2 * (warp * C::kHeads + hn)] = top;
+              ml[2 * (warp * C::kHeads + hn) + 1] = L;
+            }
           }
-          *reinterpret_cast<float4*>(red + (warp * C::kHeads + h) * C::kRedStride + 4 * d4) = O;
-          if (d4 == 0) {
-            ml[2 * (warp * C::kHeads + h)] = top;
-            ml[2 * (warp * C::kHeads + h) + 1] = L;
-          }
+          __syncthreads();
+          join4(n, nullptr);
         }
-        consumer_sync();
-        join4(true, nullptr);
       }
     }
-    consumer_sync();      // red and ml are written again by the next unit
+    // the codes' stage goes back to the copies, ml to the next unit
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
     // on to the next unit
     w.left -= n_here;
     if (w.left > 0) {
@@ -715,6 +788,11 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
         next_sequence(a, w);
       }
     }
+  }
+  if (warp == 0 && *abort_flag) {
+    // a warp has given up: wait for the copies that may still be in flight
+    for (int i = max(0, pg - C::kStages); i < pg; ++i)
+      ptx::mbar_wait_bounded(full(i % C::kStages), (i / C::kStages) & 1, nullptr, kWaitLimitNs);
   }
 }
 
