@@ -16,12 +16,13 @@
 // arrives last at the unit's counter joins them in the order of the tiles
 // (the result does not depend on timing) and sets the counter back to 0.
 //
-// Copies.  Tiles go to a ring in shared memory: codes by 2-D TMA (64 rows, or
-// four boxes of 16 where pages end inside a tile), swizzled so that both read
-// patterns below are free of bank conflicts; scales by 1-D bulk copies.  Four
-// warps take 16 tokens of each tile.  Warp 0 issues the copies as well: a
-// producer warp of its own would cost each of three CTAs per SM a quarter of
-// its registers, and the accumulators need them.
+// Copies.  Four warps take 16 tokens of each tile, and each warp has a ring
+// of its own in shared memory, which it fills by 16-byte cp.async and waits
+// for by itself: no barrier inside a unit, any page size that is a multiple
+// of 16 alike.  The chunks are swizzled so that both read patterns below are
+// free of bank conflicts.  (One warp issuing TMA boxes for all four was the
+// first form: with pages of 16 tokens, 16 small copies a tile, the copies alone
+// took 66 us for 162 MB; with pages of 128, 127 us for 706 MB.)
 //
 // Scores (m16n8k16, fp16 operands): A holds the queries, B the codes of 8
 // tokens, which are exact in
@@ -41,10 +42,7 @@
 // head, an eighth of the smallest tcgen05 tile, and the operands change
 // with every tile, so the tensor pipe is not what bounds this kernel.
 #include <algorithm>
-#include <mutex>
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
 #include "kv_device.cuh"
@@ -58,16 +56,17 @@ namespace {
 constexpr int kTile = 64;            // tokens of a tile
 constexpr int kWarps = 4;            // 16 tokens of a tile each
 constexpr int kThreads = 32 * kWarps;
-constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr float kLazy = 8.0f;        // the running maximum may lag by this power of two
 
 // How the 16 rows of an MMA are used: fp32 heads as hi (rows 0-7) and lo
 // (rows 8-15); up to 8 heads of a 16-bit type; up to 16 of them.
 enum Rows { kSplit = 0, kOne = 1, kTwo = 2 };
 
-__device__ unsigned int g_attn_decode_error_flags = 0;   // bit 0: a wait timed out, bit 1: a bad index
+__device__ unsigned int g_attn_decode_error_flags = 0;   // bit 1: a bad index
 
 struct DecodeArgs {
+  const int8_t* kc;
+  const int8_t* vc;
   const __half* ks;
   const __half* vs;
   const int32_t* lens;
@@ -86,15 +85,13 @@ struct Cfg {
   static constexpr int kHeads = R == kTwo ? 16 : 8;          // heads of a chunk
   static constexpr int kBlocks = D / 32;
   static constexpr int kStages = 4;
-  static constexpr int kCodes = kTile * D;                   // bytes of a tile's codes
-  static constexpr int kScales = kTile * kBlocks * 2;
+  static constexpr int kCodes = 16 * D;                      // bytes of 16 tokens' codes
+  static constexpr int kScales = 16 * kBlocks * 2;
+  static constexpr int kStage = 2 * kCodes + 2 * kScales;    // K, V, scales of K, of V
+  static constexpr int kRing = kStages * kStage;             // of one warp
   static constexpr int kPart = D + 4;                        // floats of a part's row: o, m, l
-  static constexpr int kOffV = kStages * kCodes;
-  static constexpr int kOffKs = 2 * kStages * kCodes;
-  static constexpr int kOffVs = kOffKs + kStages * kScales;
-  static constexpr int kOffMl = kOffVs + kStages * kScales;
-  static constexpr int kOffBars = kOffMl + kWarps * kHeads * 8 + kHeads * 4;
-  static constexpr int kSmem = kOffBars + 2 * kStages * 8 + 16 + 1024;
+  static constexpr int kOffMl = kWarps * kRing;
+  static constexpr int kSmem = kOffMl + kWarps * kHeads * 8 + kHeads * 4 + 16;
   static constexpr int kCtas = R == kTwo ? 2 : 3;            // per SM
 };
 
@@ -300,39 +297,21 @@ __device__ __forceinline__ float query_row(const DecodeArgs& a, int64_t at, bool
 
 template <int D, Rows R>
 __global__ void __launch_bounds__(kThreads, (Cfg<D, R>::kCtas))
-attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
-                   const __grid_constant__ CUtensorMap v_map, const DecodeArgs a) {
+attn_decode_kernel(const DecodeArgs a) {
   using C = Cfg<D, R>;
-  extern __shared__ unsigned char smem_raw[];
-  // the swizzle pattern is a function of the address: tiles on 1024 bytes
-  const uint32_t raw = ptx::smem_addr(smem_raw);
-  const uint32_t pad = (1024 - (raw & 1023)) & 1023;
-  unsigned char* smem = smem_raw + pad;
-  const uint32_t base = raw + pad;
-  auto full = [&](int s) { return base + C::kOffBars + 8u * s; };
-  auto empty = [&](int s) { return base + C::kOffBars + 8u * (C::kStages + s); };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBars + 16 * C::kStages);
-  int* last_flag = reinterpret_cast<int*>(smem + C::kOffBars + 16 * C::kStages + 4);
+  extern __shared__ __align__(128) unsigned char smem[];
+  float* ml = reinterpret_cast<float*>(smem + C::kOffMl);            // [warp][head][m, l]
+  float* top_s = ml + kWarps * C::kHeads * 2;                        // [head]
+  int* last_flag = reinterpret_cast<int*>(top_s + C::kHeads);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      ptx::mbar_init(full(s), 1);
-      ptx::mbar_init(empty(s), kWarps);
-    }
-    *abort_flag = 0;
-    ptx::fence_mbar_init();
-    ptx::prefetch_tensormap(&k_map);
-    ptx::prefetch_tensormap(&v_map);
-  }
-  __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // what only the walk and the ends of units need stays out of the registers
   // of the main loop
   __shared__ Split split_s;
-  __shared__ Walk pw_s;          // the copies' position (warp 0)
+  __shared__ Walk pw_s[kWarps];  // each warp's copies' position
   const int U = a.kv_heads * a.chunks;
   const int G = gridDim.x, cta = blockIdx.x;
   // every warp finds the CTA's first tile for itself (no hand-over): the sum
@@ -364,120 +343,103 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
     w.tile = static_cast<int>(r - static_cast<int64_t>(w.unit) * w.n);
     unit_start = -w.tile;
   }
-  if (threadIdx.x == 0) {
-    split_s = split;
-    pw_s = w;
-  }
-
-  auto fail = [&]() {
-    *abort_flag = 1;
-    atomicOr(&g_attn_decode_error_flags, 1u);
-  };
-  auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {
-    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
-    const bool got = ptx::mbar_wait_bounded(bar, parity, abort_flag, kWaitLimitNs);
-    return __all_sync(0xffffffffu, got);
-  };
+  if (threadIdx.x == 0) split_s = split;
+  if (lane == 0) pw_s[warp] = w;
+  __syncwarp();
 
   // ------------------------------- the copies -------------------------------
-  // Warp 0 issues them beside its share of the work, so they are kept short:
-  // lane 4 * i + x copies granule i of array x (codes of K, of V, scales of K,
-  // of V): the whole tile where pages hold whole tiles, else 16 tokens.  Its
-  // place in the table moves on by a tile at a time, and the page is read
-  // one tile ahead of its copies.
-  const int gran_shift = a.page % kTile == 0 ? 6 : 4;
+  // This warp's 16 tokens of the tiles ahead.  Their place in the table moves
+  // on by a tile at a time; the page is read one tile ahead of its copies.
   const int step_page = kTile / a.page, step_off = kTile % a.page;
-  int pg = 0;                   // tiles issued
+  const uint32_t ring = ptx::smem_addr(smem) + warp * C::kRing;
+  // chunk (of 16 bytes) lane + 32 i of the codes: row (lane + 32 i) / (D / 16),
+  // exchanged within the row's 128 (or 64) bytes
+  constexpr int kRowChunks = D / 16;
+  auto swz = [](int r) { return D == 128 ? r & 7 : (r >> 1) & 3; };
+  const int r0 = lane / kRowChunks;
+  const uint32_t to0 = r0 * D + (((lane % kRowChunks) ^ swz(r0)) << 4);
+  int p_s = 0;                  // ring slot of the next tile
   int p_left = 0;               // tiles of the unit not issued yet (0: none is left at all)
-  int p_rem = 0;                // tokens from the next tile on
-  int p_idx = 0, p_off = 0;     // this lane's granule: column of the table, token in the page
+  int p_rem = 0;                // this warp's tokens from the next tile on, the other warps' included
+  int p_idx = 0, p_off = 0;     // column of the table, token in the page
   int p_page = 0;
+  int p_head = 0;
   const int32_t* p_table = nullptr;
-  auto read_page = [&]() {
-    if (((lane >> 2) << gran_shift) < min(p_rem, kTile)) p_page = __ldg(p_table + p_idx);
-  };
   auto begin_unit = [&]() {     // from pw_s, at some tile of a unit
-    const Walk pw = pw_s;
+    const Walk pw = pw_s[warp];
     p_left = static_cast<int>(min(static_cast<int64_t>(pw.n - pw.tile), pw.left));
     if (p_left <= 0) return;
-    const int64_t pos0 = static_cast<int64_t>(pw.tile) * kTile;
-    const int pos = static_cast<int>(pos0) + ((lane >> 2) << gran_shift);
+    const int64_t pos0 = static_cast<int64_t>(pw.tile) * kTile + 16 * warp;
     p_rem = static_cast<int>(clamp_len(a, pw.b) - pos0);
-    p_idx = pos / a.page;
-    p_off = pos % a.page;
+    p_idx = static_cast<int>(pos0) / a.page;
+    p_off = static_cast<int>(pos0) % a.page;
+    p_head = pw.unit / a.chunks;
     p_table = a.table + static_cast<int64_t>(pw.b) * a.max_pages;
-    read_page();
+    if (p_rem > 0) p_page = __ldg(p_table + p_idx);
   };
   auto issue = [&]() {
-    if (p_left == 0) return;
-    const int s = pg % C::kStages;
-    if (!warp_wait(empty(s), ((pg / C::kStages) & 1) ^ 1)) {
-      fail();
-      p_left = 0;
-      return;
-    }
-    const int n = (min(p_rem, kTile) + (1 << gran_shift) - 1) >> gran_shift;    // granules with tokens
-    if (lane == 0) ptx::mbar_arrive_expect_tx(full(s), (n << gran_shift) * (2 * D + 4 * C::kBlocks));
-    __syncwarp();
-    const int gi = lane >> 2, arr = lane & 3;
-    if (gi < n) {
-      if (p_page < 0 || p_page >= a.n_pages) {
-        atomicOr(&g_attn_decode_error_flags, 2u);
-        p_page = 0;
+    if (p_left > 0) {
+      if (p_rem > 0) {
+        if (p_page < 0 || p_page >= a.n_pages) {
+          if (lane == 0) atomicOr(&g_attn_decode_error_flags, 2u);
+          p_page = 0;
+        }
+        const int64_t row = (p_page * a.kv_heads + p_head) * a.page + p_off;     // below 2^31
+        const int8_t* k = a.kc + row * D + 16 * lane;
+        const int8_t* v = a.vc + row * D + 16 * lane;
+        const uint32_t to = ring + p_s * C::kStage;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          // 4 rows of 128 bytes, or 8 of 64, further on: the exchange differs
+          // by a constant
+          const uint32_t t = to + (to0 ^ (D == 128 ? (i & 1) << 6 : 0)) + 512 * i;
+          ptx::cp_async_16(t, k + 512 * i, 16);
+          ptx::cp_async_16(t + C::kCodes, v + 512 * i, 16);
+        }
+        constexpr int kN = C::kScales / 16;
+        if (lane < 2 * kN)
+          ptx::cp_async_16(to + 2 * C::kCodes + 16 * lane,
+                           reinterpret_cast<const uint8_t*>((lane < kN ? a.ks : a.vs) + row * C::kBlocks) + 16 * (lane % kN), 16);
       }
-      const int row = (p_page * a.kv_heads + pw_s.unit / a.chunks) * a.page + p_off;
-      const int tok = gi << gran_shift;
-      if (arr < 2)
-        ptx::tma_load_2d(base + s * C::kCodes + tok * D + arr * C::kOffV, arr == 0 ? &k_map : &v_map, 0, row, full(s));
-      else
-        ptx::bulk_load(base + s * C::kScales + tok * 2 * C::kBlocks + (arr == 2 ? C::kOffKs : C::kOffVs),
-                       (arr == 2 ? a.ks : a.vs) + static_cast<int64_t>(row) * C::kBlocks,
-                       2 * C::kBlocks << gran_shift, full(s));
-    }
-    ++pg;
-    if (--p_left > 0) {
-      p_rem -= kTile;
-      p_idx += step_page;
-      p_off += step_off;
-      if (p_off >= a.page) {
-        p_off -= a.page;
-        ++p_idx;
+      p_s = p_s + 1 == C::kStages ? 0 : p_s + 1;
+      if (--p_left > 0) {
+        p_rem -= kTile;
+        p_idx += step_page;
+        p_off += step_off;
+        if (p_off >= a.page) {
+          p_off -= a.page;
+          ++p_idx;
+        }
+        if (p_rem > 0) p_page = __ldg(p_table + p_idx);
+      } else {
+        Walk pw = pw_s[warp];
+        const int here = static_cast<int>(min(static_cast<int64_t>(pw.n - pw.tile), pw.left));
+        pw.tile += here - 1;
+        pw.left -= here - 1;
+        advance(a, pw, U);
+        __syncwarp();
+        if (lane == 0) pw_s[warp] = pw;
+        __syncwarp();
+        begin_unit();
       }
-      read_page();
-    } else {
-      Walk pw = pw_s;
-      const int here = static_cast<int>(min(static_cast<int64_t>(pw.n - pw.tile), pw.left));
-      pw.tile += here - 1;
-      pw.left -= here - 1;
-      advance(a, pw, U);
-      __syncwarp();
-      if (lane == 0) pw_s = pw;
-      __syncwarp();
-      begin_unit();
     }
+    ptx::cp_async_commit();      // one group a tile, empty ones included
   };
-  if (warp == 0) {
-    __syncwarp();
-    begin_unit();
-    for (int i = 0; i < C::kStages; ++i) issue();
-  }
+  begin_unit();
+  for (int i = 0; i < C::kStages - 1; ++i) issue();
 
-  // -------------------------------- consumers -------------------------------
+  // -------------------------------- the tokens -------------------------------
   const int gq = lane >> 2, j = lane & 3;
   // Token order inside a tile of 8: column n of the score MMA is token
   // perm(n).  It makes the four rows that a half-warp reads (K), and the
   // four that the lanes j read (V), fall on different banks.
   constexpr uint32_t kPerm = D == 128 ? 0x57136420u : 0x67235410u;
   auto perm = [](int n) { return static_cast<int>((kPerm >> (4 * n)) & 7u); };
-  auto swz = [](int r) { return D == 128 ? r : (r >> 1) & 3; };   // chunk xor of row r
   const int tk = perm(gq), ta = perm(2 * j), tb = perm(2 * j + 1);
-  const uint32_t off_k = (16 * warp + tk) * D + (((j >> 1) ^ swz(tk)) << 4) + (j & 1) * 8;
-  const uint32_t off_va = (16 * warp + ta) * D + (((gq >> 2) ^ swz(ta)) << 4) + (gq & 3) * 4;
-  const uint32_t off_vb = (16 * warp + tb) * D + (((gq >> 2) ^ swz(tb)) << 4) + (gq & 3) * 4;
+  const uint32_t off_k = tk * D + (((j >> 1) ^ swz(tk)) << 4) + (j & 1) * 8;
+  const uint32_t off_va = ta * D + (((gq >> 2) ^ swz(ta)) << 4) + (gq & 3) * 4;
+  const uint32_t off_vb = tb * D + (((gq >> 2) ^ swz(tb)) << 4) + (gq & 3) * 4;
   constexpr int kH = R == kTwo ? 2 : 1;      // heads of this lane: gq, and gq + 8
-
-  float* ml = reinterpret_cast<float*>(smem + C::kOffMl);            // [warp][head][m, l]
-  float* top_s = ml + kWarps * C::kHeads * 2;                        // [head]
 
   // sequences without tokens: zeros
   for (int b = cta; b < a.B; b += G) {
@@ -491,8 +453,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
     }
   }
 
-  bool dead = false;
-  int g = 0;
+  int g_s = 0;                  // ring slot of the next tile to be used
   while (w.left > 0) {
     // ------------------------- one unit (or a part of it) -------------------------
     const int b = w.b, hk = w.unit / a.chunks, chunk = w.unit - hk * a.chunks;
@@ -522,17 +483,14 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
     for (int h = 0; h < kH; ++h) m[h] = -INFINITY, l[h] = 0.0f;
 
     const int n_here = static_cast<int>(min(static_cast<int64_t>(unit_n - tile0), w.left));
-    for (int t = n_here; t > 0; --t, ++g, rem -= kTile) {
-      const int s = g % C::kStages;
-      if (!dead && !warp_wait(full(s), (g / C::kStages) & 1)) {
-        fail();
-        dead = true;
-      }
-      const int valid = rem - 16 * warp;       // this warp's tokens (16 or more: all)
-      if (!dead && valid > 0) {
-        const uint32_t kb = base + s * C::kCodes, vb = kb + C::kOffV;
-        const uint32_t ksb = base + C::kOffKs + s * C::kScales + 16 * warp * 2 * C::kBlocks;
-        const uint32_t vsb = ksb + (C::kOffVs - C::kOffKs);
+    for (int t = n_here; t > 0; --t, rem -= kTile) {
+      issue();                                  // into the slot of the tile before
+      ptx::cp_async_wait<C::kStages - 1>();
+      __syncwarp();
+      const int valid = rem - 16 * warp;        // this warp's tokens (16 or more: all)
+      if (valid > 0) {
+        const uint32_t kb = ring + g_s * C::kStage, vb = kb + C::kCodes;
+        const uint32_t ksb = kb + 2 * C::kCodes, vsb = ksb + C::kScales;
         // ---- scores of the lane's tokens ta, tb, 8 + ta, 8 + tb
         float p[kH][4];
 #pragma unroll
@@ -651,22 +609,19 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(empty(s));
-      // refill the stage of the tile before this one: the other warps have
-      // most likely left it
-      if (warp == 0 && g > 0) issue();
+      __syncwarp();                             // all lanes have left the slot
+      g_s = g_s + 1 == C::kStages ? 0 : g_s + 1;
     }
 
     // ------------------ the four warps' parts of the unit, joined ------------------
-    // Eight heads at a time, in the codes of the tile just used: its stage is
-    // filled again only after the next tile.  Row (warp, head) holds D floats,
-    // its float4s exchanged by the head so that the four heads that lanes j
-    // write fall on different banks.
-    const int s_last = (g - 1) % C::kStages;
+    // Eight heads at a time, in the codes of the warp's slot that was used last:
+    // it is filled again only by the next tile's issue.  Row (warp, head)
+    // holds D floats, its float4s exchanged by the head so that the four heads
+    // that lanes j write fall on different banks.
+    const int s_last = g_s == 0 ? C::kStages - 1 : g_s - 1;
     auto red = [&](int x, int h, int d4) -> float4* {
-      unsigned char* at = smem + s_last * C::kCodes + (x >> 1) * C::kOffV;
-      return reinterpret_cast<float4*>(at) + (((x & 1) * 8 + h) * (D / 4) + (d4 ^ (((h >> 1) & 3) << 1)));
+      unsigned char* at = smem + x * C::kRing + s_last * C::kStage;
+      return reinterpret_cast<float4*>(at) + (h * (D / 4) + (d4 ^ (((h >> 1) & 3) << 1)));
     };
     constexpr int kVecs = D / 4;
     // Sum of the four warps' rows of heads 8 n + h; the result, or a part.
@@ -775,9 +730,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
         }
       }
     }
-    // the codes' stage goes back to the copies, ml to the next unit
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncthreads();
+    __syncthreads();      // the slot goes back to the copies, ml to the next unit
     // on to the next unit
     w.left -= n_here;
     if (w.left > 0) {
@@ -789,48 +742,11 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap k_map,
       }
     }
   }
-  if (warp == 0 && *abort_flag) {
-    // a warp has given up: wait for the copies that may still be in flight
-    for (int i = max(0, pg - C::kStages); i < pg; ++i)
-      ptx::mbar_wait_bounded(full(i % C::kStages), (i / C::kStages) & 1, nullptr, kWaitLimitNs);
-  }
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
-// The codes as [all rows][D] bytes, boxes of `gran` rows.
-bool code_map(CUtensorMap* map, int8_t* codes, const nvq_kv_cache& c, int gran) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-  if (encode == nullptr) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.head_dim),
-                              static_cast<cuuint64_t>(c.n_pages * c.n_kv_heads * c.page_size)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.head_dim)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(c.head_dim), static_cast<cuuint32_t>(gran)};
-  const cuuint32_t estr[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE,
-                c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, Rows R>
 cudaError_t decode_launch(const nvq_kv_cache& c, DecodeArgs a, cudaStream_t stream) {
   using C = Cfg<D, R>;
-  CUtensorMap k_map, v_map;
-  const int gran = c.page_size % kTile == 0 ? kTile : 16;
-  if (!code_map(&k_map, c.k_codes, c, gran) || !code_map(&v_map, c.v_codes, c, gran))
-    return cudaErrorInvalidValue;
   static SmemAttrOnce attr;
   cudaError_t e = attr.ensure(attn_decode_kernel<D, R>, C::kSmem);
   if (e != cudaSuccess) return e;
@@ -850,7 +766,7 @@ cudaError_t decode_launch(const nvq_kv_cache& c, DecodeArgs a, cudaStream_t stre
   pdl.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &pdl;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, R>, k_map, v_map, a);
+  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, R>, a);
 }
 
 }  // namespace
@@ -867,6 +783,8 @@ cudaError_t launch_attn_decode(const nvq_kv_cache& c, const int32_t* seq_lens,
                                int dtype, void* out, int64_t out_stride, int32_t* counters,
                                void* workspace, cudaStream_t stream) {
   DecodeArgs a = {};
+  a.kc = c.k_codes;
+  a.vc = c.v_codes;
   a.ks = reinterpret_cast<const __half*>(c.k_scales);
   a.vs = reinterpret_cast<const __half*>(c.v_scales);
   a.lens = seq_lens;
