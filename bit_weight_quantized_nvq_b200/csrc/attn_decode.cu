@@ -56,6 +56,7 @@ namespace {
 constexpr int kTile = 64;            // tokens of a tile
 constexpr int kWarps = 4;            // 16 tokens of a tile each
 constexpr int kThreads = 32 * kWarps;
+constexpr int kUnitCost = 3;         // a unit's start and end, in tiles
 constexpr float kLazy = 8.0f;        // the running maximum may lag by this power of two
 
 // How the 16 rows of an MMA are used: fp32 heads as hi (rows 0-7) and lo
@@ -91,74 +92,76 @@ struct Cfg {
   static constexpr int kRing = kStages * kStage;             // of one warp
   static constexpr int kPart = D + 4;                        // floats of a part's row: o, m, l
   static constexpr int kOffMl = kWarps * kRing;
-  static constexpr int kSmem = kOffMl + kWarps * kHeads * 8 + kHeads * 4 + 16;
+  static constexpr int kSmem = kOffMl + kWarps * kHeads * 8;
   static constexpr int kCtas = R == kTwo ? 2 : 3;            // per SM
 };
 
-// Tiles of all units in order: sequence by sequence, unit by unit.
+// The work in order: sequence by sequence, unit by unit, each as kUnitCost
+// places for its start and end and then one for each tile, so that a CTA that
+// gets many short units gets fewer tiles.
 struct Walk {
-  int b, unit, tile, n;      // position; n: tiles of a unit of sequence b
-  int64_t left;              // tiles of this CTA from here on, this one included
+  int b, unit, at, n;      // sequence, unit in it, place in the unit; n: the unit's tiles
+  int left;                // places of this CTA from here on
+  // tiles of the unit that are this CTA's: [first, last)
+  __device__ int first() const { return max(0, at - kUnitCost); }
+  __device__ int last() const { return max(0, min(n + kUnitCost, at + left) - kUnitCost); }
 };
 
-__device__ __forceinline__ int64_t clamp_len(const DecodeArgs& a, int b) {
-  const int64_t len = __ldg(a.lens + b), cap = static_cast<int64_t>(a.max_pages) * a.page;
-  return len < 0 ? 0 : len > cap ? cap : len;
+__device__ __forceinline__ int clamp_len(const DecodeArgs& a, int b) {
+  return max(0, min(__ldg(a.lens + b), a.max_pages * a.page));
 }
 __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b) {
-  return static_cast<int>((clamp_len(a, b) + kTile - 1) / kTile);
+  return static_cast<int>((clamp_len(a, b) + int64_t{kTile - 1}) / kTile);
 }
+__device__ __forceinline__ int places(int tiles) { return tiles > 0 ? tiles + kUnitCost : 0; }
 
-// Split of W tiles over G CTAs: the first W % G have one more.
+// Split of W places over G CTAs: the first W % G have one more.
 struct Split {
-  int64_t base, rem;
-  __device__ int64_t start(int64_t c) const { return c * base + (c < rem ? c : rem); }
-  __device__ int owner(int64_t t) const {
-    const int64_t big = rem * (base + 1);
-    return static_cast<int>(t < big ? t / (base + 1) : rem + (t - big) / base);
+  unsigned base, rem;
+  __device__ int start(int c) const { return c * base + min(static_cast<unsigned>(c), rem); }
+  __device__ int owner(int at) const {
+    const unsigned x = at, big = rem * (base + 1);
+    return x < big ? x / (base + 1) : rem + (x - big) / base;
   }
 };
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
+__device__ __forceinline__ int warp_sum_int(int v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ int64_t warp_scan64(int64_t v, int lane) {   // inclusive
+__device__ __forceinline__ int warp_scan_int(int v, int lane) {   // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   return v;
 }
 
-// On to the next sequence with tokens (there is one while tiles are left).
-__device__ __forceinline__ void next_sequence(const DecodeArgs& a, Walk& w) {
+// On to the next unit.
+__device__ __forceinline__ void next_unit(const DecodeArgs& a, Walk& w, int U) {
+  w.left -= w.n + kUnitCost - w.at;
+  w.at = 0;
+  if (w.left <= 0 || ++w.unit < U) return;
+  w.unit = 0;
   do {
-    if (++w.b >= a.B) {
+    if (++w.b >= a.B) {     // not met while places are left
       w.left = 0;
       return;
     }
     w.n = tiles_of(a, w.b);
   } while (w.n == 0);
 }
-__device__ __forceinline__ void advance(const DecodeArgs& a, Walk& w, int U) {
-  if (--w.left <= 0) return;
-  if (++w.tile < w.n) return;
-  w.tile = 0;
-  if (++w.unit < U) return;
-  w.unit = 0;
-  next_sequence(a, w);
-}
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
+                                        float c2, float c3) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -205,27 +208,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// Eight consecutive elements of a row.
-__device__ __forceinline__ void load8(const void* p, int64_t at, int dtype, float (&x)[8]) {
-  if (dtype == NVQ_F32) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 u = __ldg(s), v = __ldg(s + 1);
-    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-    return;
-  }
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (dtype == NVQ_F16) {
-      const float2 f = __half22float2(dev::bits_h2(w[i]));
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
-    } else {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-}
 __device__ __forceinline__ void store4(void* p, int64_t at, int dtype, float4 v) {
   if (dtype == NVQ_F32) {
     *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = v;
@@ -239,26 +221,54 @@ __device__ __forceinline__ void store4(void* p, int64_t at, int dtype, float4 v)
   }
 }
 
-// One query row's values of this lane (8 per block: 32 * block + 8 * j ..) as
-// A fragments: scaled by a power of two so that the row's largest lies in
+// The words of a query row that lane j holds: 8 elements of each block, at
+// 32 * block + 8 * j; zeros for a row that is none.
+template <int D, bool F32>
+struct Raw {
+  uint4 w[D / 32 * (F32 ? 2 : 1)];
+  __device__ __forceinline__ void load(const void* q, int64_t at, bool on, int j) {
+#pragma unroll
+    for (int bl = 0; bl < D / 32; ++bl) {
+      if (F32) {
+        const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(q) + at + 32 * bl + 8 * j);
+        w[2 * bl] = on ? __ldg(s) : make_uint4(0, 0, 0, 0);
+        w[(2 * bl + 1) % (sizeof(w) / 16)] = on ? __ldg(s + 1) : make_uint4(0, 0, 0, 0);
+      } else {
+        w[bl] = on ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(q) + at + 32 * bl + 8 * j))
+                   : make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void values(int dtype, float (&x)[D / 4]) const {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(w) / 16); ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (F32) {
+          x[(4 * i + k) % (D / 4)] = __uint_as_float(u[k]);
+        } else {
+          const float2 f = dtype == NVQ_F16 ? __half22float2(dev::bits_h2(u[k]))
+                                            : make_float2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xFFFF0000u));
+          x[(8 * i + 2 * k) % (D / 4)] = f.x, x[(8 * i + 2 * k + 1) % (D / 4)] = f.y;
+        }
+      }
+    }
+  }
+};
+
+// The row as operands: scaled by a power of two so that its largest lies in
 // [2^13, 2^14), then rounded to fp16, and the remainder for `lo`.  Returns
 // the factor that turns the MMA's sums into powers of two; `start` is what the
 // sums over each block begin with, -128 * 2^-24 * sum of the operands.
-template <int D, bool LO>
-__device__ __forceinline__ float query_row(const DecodeArgs& a, int64_t at, bool on, int j,
+template <int D, bool F32, bool LO>
+__device__ __forceinline__ float query_row(const Raw<D, F32>& raw, int dtype, float scale_log2,
                                            uint32_t (&hi)[D / 8], uint32_t (&lo)[D / 8],
                                            float (&start)[D / 32], float (&start_lo)[D / 32]) {
   float x[D / 4], top = 0.0f;
+  raw.values(dtype, x);
 #pragma unroll
-  for (int bl = 0; bl < D / 32; ++bl) {
-    float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (on) load8(a.q, at + 32 * bl + 8 * j, a.dtype, y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[8 * bl + i] = y[i];
-      top = fmaxf(top, fabsf(y[i]));
-    }
-  }
+  for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
   // 2^(13 - exponent), kept within fp32's normal range (zeros and subnormals)
@@ -292,7 +302,7 @@ __device__ __forceinline__ float query_row(const DecodeArgs& a, int64_t at, bool
     }
   }
   // 2^24 (the codes' unit) and 2^-k; k > -128 + 24 even for infinities
-  return a.scale_log2 * 0x1p24f * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  return scale_log2 * 0x1p24f * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
 }
 
 template <int D, Rows R>
@@ -301,8 +311,6 @@ attn_decode_kernel(const DecodeArgs a) {
   using C = Cfg<D, R>;
   extern __shared__ __align__(128) unsigned char smem[];
   float* ml = reinterpret_cast<float*>(smem + C::kOffMl);            // [warp][head][m, l]
-  float* top_s = ml + kWarps * C::kHeads * 2;                        // [head]
-  int* last_flag = reinterpret_cast<int*>(top_s + C::kHeads);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -310,38 +318,46 @@ attn_decode_kernel(const DecodeArgs a) {
 
   // what only the walk and the ends of units need stays out of the registers
   // of the main loop
+  struct Seg {
+    int b, unit, n, start;      // a unit that other CTAs have parts of; start: its first place
+  };
   __shared__ Split split_s;
   __shared__ Walk pw_s[kWarps];  // each warp's copies' position
+  __shared__ Seg seg_s[2];
+  __shared__ int last_s[2];
   const int U = a.kv_heads * a.chunks;
   const int G = gridDim.x, cta = blockIdx.x;
-  // every warp finds the CTA's first tile for itself (no hand-over): the sum
-  // of all tiles, then the sequence that holds the first one
-  int64_t total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) total += b0 + lane < a.B ? tiles_of(a, b0 + lane) : 0;
-  total = warp_sum64(total) * U;
-  const Split split = {total / G, total % G};
-  const int64_t first = split.start(cta);
-  Walk w = {0, 0, 0, 1, split.start(cta + 1) - first};
-  int64_t unit_start = 0;       // the first tile of the unit of `w`, counted from the CTA's first
+  // every warp finds the CTA's first place for itself (no hand-over): the sum
+  // of all places, then the sequence that holds the first one
+  int total = 0, mine = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    mine = b0 + lane < a.B ? tiles_of(a, b0 + lane) : 0;
+    total += places(mine);
+  }
+  total = warp_sum_int(total) * U;
+  const Split split = {static_cast<unsigned>(total) / G, static_cast<unsigned>(total) % G};
+  Walk w = {0, 0, 0, 0, split.start(cta + 1) - split.start(cta)};
+  int unit_start = 0;           // the first place of the unit of `w`
   if (w.left > 0) {
-    int64_t before = 0;
+    const int first = split.start(cta);
+    int before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int64_t mine = b0 + lane < a.B ? tiles_of(a, b0 + lane) : 0;
-      const int64_t incl = warp_scan64(mine, lane);
+      if (a.B > 32) mine = b0 + lane < a.B ? tiles_of(a, b0 + lane) : 0;
+      const int incl = warp_scan_int(places(mine), lane);
       const unsigned hit = __ballot_sync(0xffffffffu, (before + incl) * U > first);
       if (hit != 0) {
         const int at = __ffs(hit) - 1;
         w.b = b0 + at;
-        w.n = static_cast<int>(__shfl_sync(0xffffffffu, mine, at));
-        before += __shfl_sync(0xffffffffu, incl - mine, at);
+        w.n = __shfl_sync(0xffffffffu, mine, at);
+        before += __shfl_sync(0xffffffffu, incl - places(mine), at);
         break;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    const int64_t r = first - before * U;
-    w.unit = static_cast<int>(r / w.n);
-    w.tile = static_cast<int>(r - static_cast<int64_t>(w.unit) * w.n);
-    unit_start = -w.tile;
+    const int r = first - before * U;
+    w.unit = static_cast<unsigned>(r) / static_cast<unsigned>(w.n + kUnitCost);
+    w.at = r - w.unit * (w.n + kUnitCost);
+    unit_start = first - w.at;
   }
   if (threadIdx.x == 0) split_s = split;
   if (lane == 0) pw_s[warp] = w;
@@ -367,12 +383,15 @@ attn_decode_kernel(const DecodeArgs a) {
   const int32_t* p_table = nullptr;
   auto begin_unit = [&]() {     // from pw_s, at some tile of a unit
     const Walk pw = pw_s[warp];
-    p_left = static_cast<int>(min(static_cast<int64_t>(pw.n - pw.tile), pw.left));
-    if (p_left <= 0) return;
-    const int64_t pos0 = static_cast<int64_t>(pw.tile) * kTile + 16 * warp;
-    p_rem = static_cast<int>(clamp_len(a, pw.b) - pos0);
-    p_idx = static_cast<int>(pos0) / a.page;
-    p_off = static_cast<int>(pos0) % a.page;
+    p_left = pw.left > 0 ? pw.last() - pw.first() : 0;
+    if (p_left <= 0) {
+      p_left = 0;
+      return;
+    }
+    const int pos0 = pw.first() * kTile + 16 * warp;
+    p_rem = clamp_len(a, pw.b) - pos0;
+    p_idx = pos0 / a.page;
+    p_off = pos0 % a.page;
     p_head = pw.unit / a.chunks;
     p_table = a.table + static_cast<int64_t>(pw.b) * a.max_pages;
     if (p_rem > 0) p_page = __ldg(p_table + p_idx);
@@ -413,10 +432,7 @@ attn_decode_kernel(const DecodeArgs a) {
         if (p_rem > 0) p_page = __ldg(p_table + p_idx);
       } else {
         Walk pw = pw_s[warp];
-        const int here = static_cast<int>(min(static_cast<int64_t>(pw.n - pw.tile), pw.left));
-        pw.tile += here - 1;
-        pw.left -= here - 1;
-        advance(a, pw, U);
+        next_unit(a, pw, U);
         __syncwarp();
         if (lane == 0) pw_s[warp] = pw;
         __syncwarp();
@@ -453,23 +469,73 @@ attn_decode_kernel(const DecodeArgs a) {
     }
   }
 
+  Raw<D, R == kSplit> raw[kH];
+  auto load_queries = [&]() {
+    const int hk = w.unit / a.chunks, chunk = w.unit - hk * a.chunks;
+    const int hc = min(C::kHeads, a.group - chunk * C::kHeads);
+    const int64_t at = w.b * a.q_stride + static_cast<int64_t>(hk * a.group + chunk * C::kHeads) * D;
+#pragma unroll
+    for (int h = 0; h < kH; ++h) raw[h].load(a.q, at + (gq + 8 * h) * D, gq + 8 * h < hc, j);
+  };
+  constexpr int kVecs = D / 4;
+  int s_last = 0;               // ring slot used last
+  // Row (warp x, head h) of eight heads' sums, in the codes of the ring slot
+  // that was used last (it is filled again only by the next tile's issue):
+  // D floats, its float4s exchanged by the head so that the four heads that
+  // lanes j write fall on different banks.
+  auto red = [&](int x, int h, int d4) -> float4* {
+    unsigned char* at = smem + x * C::kRing + s_last * C::kStage;
+    return reinterpret_cast<float4*>(at) + (h * (D / 4) + (d4 ^ (((h >> 1) & 3) << 1)));
+  };
+  // Sum of the four warps' rows of the chunk's heads 8 n + h; the result, or a part.
+  auto join4 = [&](int b, int unit, int n, float* part) {
+    const int hk = unit / a.chunks, chunk = unit - hk * a.chunks;
+    const int hc = min(C::kHeads, a.group - chunk * C::kHeads);
+    const int64_t to_out = b * a.out_stride + static_cast<int64_t>(hk * a.group + chunk * C::kHeads) * D;
+    for (int i = threadIdx.x; i < min(8, hc - 8 * n) * kVecs; i += kThreads) {
+      const int h = i / kVecs, d4 = i - h * kVecs, hn = 8 * n + h;
+      float top = -INFINITY, L = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) top = fmaxf(top, ml[2 * (x * C::kHeads + hn)]);
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) {
+        const float mx = ml[2 * (x * C::kHeads + hn)];
+        const float c = mx == -INFINITY ? 0.0f : exp2_approx(mx - top);
+        L = fmaf(c, ml[2 * (x * C::kHeads + hn) + 1], L);
+        const float4 v = *red(x, h, d4);
+        O.x = fmaf(c, v.x, O.x), O.y = fmaf(c, v.y, O.y), O.z = fmaf(c, v.z, O.z), O.w = fmaf(c, v.w, O.w);
+      }
+      if (part == nullptr) {
+        const float inv = __fdividef(1.0f, L);
+        store4(a.out, to_out + hn * D + 4 * d4, a.dtype, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
+      } else {
+        float* to = part + hn * C::kPart;
+        __stcg(reinterpret_cast<float4*>(to + 4 * d4), O);
+        if (d4 == 0) __stcg(reinterpret_cast<float2*>(to + D), make_float2(top, L));
+      }
+    }
+  };
+  const int64_t part_floats = static_cast<int64_t>(a.rows) * C::kPart;
+
   int g_s = 0;                  // ring slot of the next tile to be used
+  int segs = 0;                 // units here that other CTAs have parts of
+  if (w.left > 0 && w.last() <= w.first()) w.left = 0;      // places of a unit's cost alone
   while (w.left > 0) {
     // ------------------------- one unit (or a part of it) -------------------------
-    const int b = w.b, hk = w.unit / a.chunks, chunk = w.unit - hk * a.chunks;
-    const int unit_n = w.n, tile0 = w.tile, unit = w.unit;
-    const int hc = min(C::kHeads, a.group - chunk * C::kHeads);      // heads of this chunk
-    const int h0 = hk * a.group + chunk * C::kHeads;
+    const int b = w.b, unit = w.unit, tile0 = w.first(), n_here = w.last() - tile0;
+    const bool whole = n_here == w.n;
     // tokens from the first tile of this part on; only the last tile's matter
-    int rem = static_cast<int>(min(clamp_len(a, b) - static_cast<int64_t>(tile0) * kTile, int64_t{INT32_MAX}));
+    int rem = clamp_len(a, b) - tile0 * kTile;
+    load_queries();
     uint32_t qh[D / 8], ql[D / 8];
     float factor[kH];
     float start[C::kBlocks], start2[C::kBlocks];       // of rows gq and gq + 8
-    factor[0] = query_row<D, R == kSplit>(a, b * a.q_stride + static_cast<int64_t>(h0 + gq) * D, gq < hc, j, qh, ql, start, start2);
-    if (R == kTwo) {
+    factor[0] = query_row<D, R == kSplit, R == kSplit>(raw[0], a.dtype, a.scale_log2, qh, ql, start, start2);
+    if constexpr (R == kTwo) {
       uint32_t none[D / 8];
       float unused[C::kBlocks];
-      factor[kH - 1] = query_row<D, false>(a, b * a.q_stride + static_cast<int64_t>(h0 + gq + 8) * D, gq + 8 < hc, j, ql, none, start2, unused);
+      factor[kH - 1] = query_row<D, false, false>(raw[kH - 1], a.dtype, a.scale_log2, ql, none, start2, unused);
     }
 
     // o[n][2 * bl + x]: heads 8 n + 2 j (elements 0, 2) and 8 n + 2 j + 1 (1, 3),
@@ -482,7 +548,6 @@ attn_decode_kernel(const DecodeArgs a) {
 #pragma unroll
     for (int h = 0; h < kH; ++h) m[h] = -INFINITY, l[h] = 0.0f;
 
-    const int n_here = static_cast<int>(min(static_cast<int64_t>(unit_n - tile0), w.left));
     for (int t = n_here; t > 0; --t, rem -= kTile) {
       issue();                                  // into the slot of the tile before
       ptx::cp_async_wait<C::kStages - 1>();
@@ -514,10 +579,12 @@ attn_decode_kernel(const DecodeArgs a) {
             uint32_t b0, b1, b2, b3;
             codes_to_h2(c8.x, b0, b1);
             codes_to_h2(c8.y, b2, b3);
-            float acc[4] = {start[bl], start[bl], R == kOne ? 0.f : start2[bl], R == kOne ? 0.f : start2[bl]};
+            float acc[4];
             const uint32_t z = 0;
-            mma_f16(acc, qh[4 * bl], R == kOne ? z : ql[4 * bl], qh[4 * bl + 1], R == kOne ? z : ql[4 * bl + 1], b0, b1);
-            mma_f16(acc, qh[4 * bl + 2], R == kOne ? z : ql[4 * bl + 2], qh[4 * bl + 3], R == kOne ? z : ql[4 * bl + 3], b2, b3);
+            const float c = start[bl], c2 = R == kOne ? 0.0f : start2[bl];
+            mma_f16(acc, qh[4 * bl], R == kOne ? z : ql[4 * bl], qh[4 * bl + 1], R == kOne ? z : ql[4 * bl + 1], b0, b1, c, c, c2, c2);
+            mma_f16(acc, qh[4 * bl + 2], R == kOne ? z : ql[4 * bl + 2], qh[4 * bl + 3], R == kOne ? z : ql[4 * bl + 3], b2, b3,
+                    acc[0], acc[1], acc[2], acc[3]);
             if (R == kSplit) acc[0] += acc[2], acc[1] += acc[3];
             sa[0] = fmaf(da[bl], acc[0], sa[0]);
             sb[0] = fmaf(db[bl], acc[1], sb[0]);
@@ -528,9 +595,16 @@ attn_decode_kernel(const DecodeArgs a) {
           }
 #pragma unroll
           for (int h = 0; h < kH; ++h) {
-            p[h][2 * x] = 8 * x + ta < valid ? sa[h] * factor[h] : -INFINITY;
-            p[h][2 * x + 1] = 8 * x + tb < valid ? sb[h] * factor[h] : -INFINITY;
+            p[h][2 * x] = sa[h] * factor[h];
+            p[h][2 * x + 1] = sb[h] * factor[h];
           }
+        }
+        if (valid < 16) {        // the last tile
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((i >> 1) * 8 + (i & 1 ? tb : ta) >= valid)
+#pragma unroll
+              for (int h = 0; h < kH; ++h) p[h][i] = -INFINITY;
         }
         // ---- running maximum (the same in the four lanes of a head) and sum.
         // The maximum is only a reference point: it may lag while no exponent
@@ -571,7 +645,11 @@ attn_decode_kernel(const DecodeArgs a) {
         for (int i = 0; i < 4; ++i) {
           const int tok = (i >> 1) * 8 + (i & 1 ? tb : ta);
           sc[i] = D == 128 ? lds64(vsb + tok * 8) : make_uint2(lds32(vsb + tok * 4), 0u);
-          if (tok >= valid) sc[i] = make_uint2(0u, 0u);      // whatever lies behind the last token
+        }
+        if (valid < 16) {        // whatever lies behind the last token
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((i >> 1) * 8 + (i & 1 ? tb : ta) >= valid) sc[i] = make_uint2(0u, 0u);
         }
 #pragma unroll
         for (int bl = 0; bl < C::kBlocks; ++bl) {
@@ -614,46 +692,18 @@ attn_decode_kernel(const DecodeArgs a) {
     }
 
     // ------------------ the four warps' parts of the unit, joined ------------------
-    // Eight heads at a time, in the codes of the warp's slot that was used last:
-    // it is filled again only by the next tile's issue.  Row (warp, head)
-    // holds D floats, its float4s exchanged by the head so that the four heads
-    // that lanes j write fall on different banks.
-    const int s_last = g_s == 0 ? C::kStages - 1 : g_s - 1;
-    auto red = [&](int x, int h, int d4) -> float4* {
-      unsigned char* at = smem + x * C::kRing + s_last * C::kStage;
-      return reinterpret_cast<float4*>(at) + (h * (D / 4) + (d4 ^ (((h >> 1) & 3) << 1)));
-    };
-    constexpr int kVecs = D / 4;
-    // Sum of the four warps' rows of heads 8 n + h; the result, or a part.
-    auto join4 = [&](int n, float* part) {
-      for (int i = threadIdx.x; i < min(8, hc - 8 * n) * kVecs; i += kThreads) {
-        const int h = i / kVecs, d4 = i - h * kVecs, hn = 8 * n + h;
-        float top = -INFINITY, L = 0.0f;
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x) top = fmaxf(top, ml[2 * (x * C::kHeads + hn)]);
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x) {
-          const float mx = ml[2 * (x * C::kHeads + hn)];
-          const float c = mx == -INFINITY ? 0.0f : exp2_approx(mx - top);
-          L = fmaf(c, ml[2 * (x * C::kHeads + hn) + 1], L);
-          const float4 v = *red(x, h, d4);
-          O.x = fmaf(c, v.x, O.x), O.y = fmaf(c, v.y, O.y), O.z = fmaf(c, v.z, O.z), O.w = fmaf(c, v.w, O.w);
-        }
-        if (part == nullptr) {
-          const float inv = __fdividef(1.0f, L);
-          store4(a.out, b * a.out_stride + static_cast<int64_t>(h0 + hn) * D + 4 * d4, a.dtype,
-                 make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
-        } else {
-          float* to = part + hn * C::kPart;
-          __stcg(reinterpret_cast<float4*>(to + 4 * d4), O);
-          if (d4 == 0) __stcg(reinterpret_cast<float2*>(to + D), make_float2(top, L));
-        }
-      }
-    };
-    const bool whole = n_here == unit_n;
-    const int slot = 2 * cta + (unit_start >= 0 ? 1 : 0);
-    const int64_t part_floats = static_cast<int64_t>(a.rows) * C::kPart;
+    // Eight heads at a time.  A part goes to this CTA's slot of the workspace:
+    // the second one if it starts the unit (then it is the CTA's last), else
+    // the first.
+    s_last = g_s == 0 ? C::kStages - 1 : g_s - 1;
+    float* part = whole ? nullptr : a.part + (2 * static_cast<int64_t>(cta) + (tile0 == 0 ? 1 : 0)) * part_floats;
+    if (!whole) {
+      if (threadIdx.x == 0) seg_s[segs] = {b, unit, w.n, unit_start};
+      ++segs;
+    }
+    unit_start += w.n + kUnitCost;
+    next_unit(a, w, U);
+    if (w.left > 0 && w.last() <= w.first()) w.left = 0;
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
@@ -671,75 +721,78 @@ attn_decode_kernel(const DecodeArgs a) {
         *red(warp, 2 * j + 1, 8 * bl + gq) = make_float4(u[1], u[3], v[1], v[3]);
       }
       __syncthreads();
-      join4(h, whole ? nullptr : a.part + slot * part_floats);
-    }
-    if (!whole) {
-      // the CTA that arrives last adds up the unit's parts, in tile order
-      const Split split = split_s;
-      const int64_t unit_first = split.start(cta) + unit_start;
-      const int c0 = split.owner(unit_first), c1 = split.owner(unit_first + unit_n - 1);
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        int* counter = a.counters + static_cast<int64_t>(b) * U + unit;
-        const int old = atomicAdd(counter, 1);
-        __threadfence();
-        *last_flag = old == c1 - c0;
-        if (old == c1 - c0) *counter = 0;
-      }
-      __syncthreads();
-      if (*last_flag) {
-        // only the first part can lie in a CTA's second slot: the others
-        // start where their CTA does
-        const float* first_part = a.part + (2 * static_cast<int64_t>(c0) + (unit_first >= split.start(c0) ? 1 : 0)) * part_floats;
-        const float* next_parts = a.part + 2 * (static_cast<int64_t>(c0) + 1) * part_floats;
-        auto part_of = [&](int i) { return i == 0 ? first_part : next_parts + 2 * (i - 1) * part_floats; };
-        const int parts = c1 - c0 + 1;
-        // maximum of each head over the parts, then each warp adds a quarter of them
-        for (int h = warp; h < hc; h += kWarps) {
-          float top = -INFINITY;
-          for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldcg(part_of(i) + h * C::kPart + D));
-#pragma unroll
-          for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-          if (lane == 0) top_s[h] = top;
-        }
-        for (int n = 0; n < kH; ++n) {
-          __syncthreads();
-          for (int i = lane; i < min(8, hc - 8 * n) * kVecs; i += 32) {
-            const int h = i / kVecs, d4 = i - h * kVecs, hn = 8 * n + h;
-            const float top = top_s[hn];
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-            float L = 0.0f;
-#pragma unroll 8
-            for (int x = warp; x < parts; x += kWarps) {
-              const float* from = part_of(x) + hn * C::kPart;
-              const float2 y = __ldcg(reinterpret_cast<const float2*>(from + D));
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(from + 4 * d4));
-              const float f = exp2_approx(y.x - top);
-              L = fmaf(f, y.y, L);
-              O.x = fmaf(f, v.x, O.x), O.y = fmaf(f, v.y, O.y), O.z = fmaf(f, v.z, O.z), O.w = fmaf(f, v.w, O.w);
-            }
-            *red(warp, h, d4) = O;
-            if (d4 == 0) {
-              ml[2 * (warp * C::kHeads + hn)] = top;
-              ml[2 * (warp * C::kHeads + hn) + 1] = L;
-            }
-          }
-          __syncthreads();
-          join4(n, nullptr);
-        }
-      }
+      join4(b, unit, h, part);
     }
     __syncthreads();      // the slot goes back to the copies, ml to the next unit
-    // on to the next unit
-    w.left -= n_here;
-    if (w.left > 0) {
-      unit_start += unit_n;
-      w.tile = 0;
-      if (++w.unit == U) {
-        w.unit = 0;
-        next_sequence(a, w);
+  }
+
+  // ----------------------- units that several CTAs have parts of -----------------------
+  // All arrivals are made here, so that no stream of copies waits for one; the
+  // CTA that arrives last adds up the unit's parts, in tile order.
+  if (segs == 0) return;
+  const Split sp = split_s;
+  auto owners = [&](const Seg& x, int& c0, int& c1) {
+    c0 = sp.owner(x.start + kUnitCost);
+    c1 = sp.owner(x.start + kUnitCost + x.n - 1);
+  };
+  if (threadIdx.x < segs) {
+    const Seg x = seg_s[threadIdx.x];
+    int c0, c1;
+    owners(x, c0, c1);
+    int* counter = a.counters + static_cast<int64_t>(x.b) * U + x.unit;
+    __threadfence();      // the parts of this CTA, seen through the barrier, come first
+    const int old = atomicAdd(counter, 1);
+    __threadfence();
+    last_s[threadIdx.x] = old == c1 - c0;
+    if (old == c1 - c0) *counter = 0;
+  }
+  __syncthreads();
+  for (int i = 0; i < segs; ++i) {
+    if (!last_s[i]) continue;
+    const Seg x = seg_s[i];
+    int c0, c1;
+    owners(x, c0, c1);
+    const int parts = c1 - c0 + 1, chunk = x.unit % a.chunks;
+    const int hc = min(C::kHeads, a.group - chunk * C::kHeads);
+    const float* from = a.part + (2 * static_cast<int64_t>(c0) + 1) * part_floats;      // part 0, then every second slot from c0 + 1 on
+    for (int n = 0; n < kH; ++n) {
+      // each warp adds a quarter of the parts, every load of eight of them at once
+      for (int e = lane; e < min(8, hc - 8 * n) * kVecs; e += 32) {
+        const int h = e / kVecs, d4 = e - h * kVecs, hn = 8 * n + h;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        float top = -INFINITY, L = 0.0f;
+        for (int k0 = warp; k0 < parts; k0 += 8 * kWarps) {
+          float2 y[8];
+          float4 v[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int k = k0 + u * kWarps;
+            const float* at = from + (k == 0 ? 0 : 2 * k - 1) * part_floats + hn * C::kPart;
+            y[u] = k < parts ? __ldcg(reinterpret_cast<const float2*>(at + D)) : make_float2(-INFINITY, 0.0f);
+            v[u] = k < parts ? __ldcg(reinterpret_cast<const float4*>(at + 4 * d4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          float mn = top;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) mn = fmaxf(mn, y[u].x);
+          const float c = top == -INFINITY ? 0.0f : exp2_approx(top - mn);
+          top = mn;
+          L *= c, O.x *= c, O.y *= c, O.z *= c, O.w *= c;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const float f = y[u].x == -INFINITY ? 0.0f : exp2_approx(y[u].x - mn);
+            L = fmaf(f, y[u].y, L);
+            O.x = fmaf(f, v[u].x, O.x), O.y = fmaf(f, v[u].y, O.y), O.z = fmaf(f, v[u].z, O.z), O.w = fmaf(f, v[u].w, O.w);
+          }
+        }
+        *red(warp, h, d4) = O;
+        if (d4 == 0) {
+          ml[2 * (warp * C::kHeads + hn)] = top;
+          ml[2 * (warp * C::kHeads + hn) + 1] = L;
+        }
       }
+      __syncthreads();
+      join4(x.b, x.unit, n, nullptr);
+      __syncthreads();
     }
   }
 }

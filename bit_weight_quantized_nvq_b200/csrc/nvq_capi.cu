@@ -446,6 +446,12 @@ nvq_status nvq_attn_decode(const nvq_kv_cache* cache, const void* q, int64_t q_s
   if (st != NVQ_OK) return st;
   if (B > 65535 || max_pages > kInt32Max || max_pages * cache->page_size > kInt32Max)
     return NVQ_ERR_BAD_SHAPE;
+  // the work is counted in 32 bits: 64-token tiles of every key-value head
+  // (and chunk of 8 or 16 heads that share one), with room for their ends
+  const int64_t share = dtype == NVQ_F32 ? 8 : 16;
+  const int64_t chunks = (n_heads / cache->n_kv_heads + share - 1) / share;
+  if (B * cache->n_kv_heads * chunks > kInt32Max / (max_pages * cache->page_size / 64 + 8))
+    return NVQ_ERR_BAD_SHAPE;
   if (B == 0) return NVQ_OK;
   if (!seq_lens || (!block_table && max_pages > 0) || !counters) return NVQ_ERR_INVALID_ARG;
   const int64_t width = n_heads * cache->head_dim;
