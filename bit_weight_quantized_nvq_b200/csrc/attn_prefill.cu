@@ -3,78 +3,695 @@
 // Query i of a sequence (n queries, m keys) sees the keys j < m, with
 // `causal` only j <= i + m - n (the queries are the last n positions):
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q.k_j - max);
-// a query that sees no key gives 0.
+// a query that sees no key gives 0.  One pass over the keys with a running
+// maximum and sum.
 //
-// One warp per (row, head) with an online softmax.
+// Two bounds are equally near at head_dim 128: a block of 128 queries and 128
+// keys takes the tensor core 2 x 512 cycles (S = Q K^T and O += P V) and the
+// special-function units 1024 cycles (16384 exponentials at 16 a cycle).  So
+// a persistent CTA per SM works on two query tiles at once, and while the
+// exponentials of one are formed the tensor core has the products of the other.
+//
+//   warps 0-3   softmax of tile 0, one thread per query row: read S from
+//               tensor memory, write P = exp2(..) over it as the left operand
+//               of the next product; at the end O / sum -> out
+//   warps 4-7   the same for tile 1
+//   warp 8      issues the MMAs: per key block and tile O += P V, then the next
+//               S (a tile's S and P share their columns, so in this order)
+//   warp 9      TMA: both Q tiles, then K and V blocks into a ring
+//   warps 10-11 clean a V block that some query does not see all of (below)
+//
+// The two tiles share K and V: two heads of one key-value head with the same
+// 128 queries where the group is even, else 256 queries of one head.  Work
+// items are (sequence, tile, heads), the later tiles of a sequence (more
+// keys) first, dealt round to the CTAs.
+//
+// The running maximum is a reference point only and may lag by 2^8, so almost
+// every block needs one pass over S and no rescaling of O; where a row passes
+// that, its warp rescales O (the previous product has finished by then: S is
+// formed after it) and forms the block again.
+//
+// A key behind a query's last one gets p = 0, but 0 * NaN is not 0: before a
+// block with such keys is used, rows of V behind the sequence's end are
+// zeroed in shared memory, and NaN and infinities in rows that only some of
+// the queries see are replaced by 0 and added to those queries' results at
+// the end.
+#include <algorithm>
+#include <climits>
+#include <mutex>
+#include <type_traits>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
 #include "kv_device.cuh"
+#include "nvq_device.cuh"
 #include "nvq_internal.h"
+#include "tcgen05.cuh"
 
 namespace nvq {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kTile = 128;           // queries of a tile, keys of a block
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
+constexpr uint64_t kWaitLimitNs = 4000000000ull;
+constexpr float kLazy = 8.0f;
+constexpr int kItemFlags = 8;        // found flags of the last items
+constexpr int kRaw = 4;              // V blocks on their way to be cleaned (the ring holds fewer)
 
 __device__ unsigned int g_attn_prefill_error_flags = 0;   // bit 0: a wait timed out, bit 1: a bad index
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
-attn_prefill_kernel(PrefillArgs a, float scale_log2) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kWarps + (threadIdx.x >> 5), h = blockIdx.y;
-  if (row >= a.total_q) return;
-  const int b = dev::warp_find_seq(a.cu_q, static_cast<int>(a.B), row, lane);
-  if (b >= a.B) return;
-  const int hk = h / static_cast<int>(a.heads / a.kv_heads);
-  const int64_t k0 = a.cu_k[b];
-  int64_t m_keys = a.cu_k[b + 1] - k0;
-  const int64_t i = row - a.cu_q[b], n = a.cu_q[b + 1] - a.cu_q[b];
-  if (k0 < 0 || m_keys < 0 || k0 + m_keys > a.total_k || i < 0 || i >= n ||
-      a.cu_q[b + 1] > a.total_q) {
-    if (lane == 0) atomicOr(&g_attn_prefill_error_flags, 2u);
-    m_keys = 0;
+template <int D>
+struct Cfg {
+  static constexpr int kSub = kTile * 128;              // a 64-wide, 128-byte swizzled sub-tile
+  static constexpr int kSubs = D / 64;
+  static constexpr int kBlock = kSubs * kSub;           // bytes of a Q tile, K or V block
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kOffRing = 2 * kBlock;
+  static constexpr int kOffBars = kOffRing + kStages * kBlock;
+  static constexpr int kBars = 2 * kStages + 2 + 6 + kRaw + 1;
+  static constexpr int kOffMisc = kOffBars + 8 * kBars;
+  static constexpr int kSmem = kOffMisc + 16 + 8 * kItemFlags + 1024;
+};
+
+struct Args {
+  const void* v;
+  void* out;
+  int64_t v_stride, out_stride;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int B, total_q, total_k, group, heads, pairs, max_items;
+  float scale_log2;
+  int causal, two_heads;
+};
+
+// One item: a sequence's rows, and what each of its two tiles does.
+struct Item {
+  int q0, n, k0, m;          // packed rows of the sequence: queries, keys
+  int row[2], head[2];       // first query and head of each tile
+  int blocks[2];             // key blocks of each (0: it sees none)
+  bool on[2];                // whether the tile has queries
+  int clean_from;            // the first key that some query does not see
+  __device__ int last() const { return max(blocks[0], blocks[1]); }
+  // keys that query i (of the sequence) sees
+  __device__ int limit(int i, int causal) const { return causal ? min(m, i + m - n + 1) : m; }
+};
+
+__device__ __forceinline__ void sequence(const Args& a, int b, int& q0, int& n, int& k0, int& m) {
+  q0 = __ldg(a.cu_q + b);
+  int q1 = __ldg(a.cu_q + b + 1), k1 = __ldg(a.cu_k + b + 1);
+  k0 = __ldg(a.cu_k + b);
+  if (q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k) {
+    // no keys; the rows that lie inside give zeros
+    atomicOr(&g_attn_prefill_error_flags, 2u);
+    q0 = min(max(q0, 0), a.total_q);
+    q1 = min(max(q1, q0), a.total_q);
+    k0 = k1 = 0;
   }
-  const int64_t end = a.causal ? min(m_keys, i + m_keys - n + 1) : m_keys;
-  const T* q = static_cast<const T*>(a.q) + row * a.q_stride + h * D + lane * E;
-  float qv[E], o[E], m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) qv[e] = dev::to_f32(q[e]) * scale_log2, o[e] = 0.0f;
-  for (int64_t j = 0; j < end; ++j) {
-    const T* k = static_cast<const T*>(a.k) + (k0 + j) * a.k_stride + hk * D + lane * E;
-    const T* v = static_cast<const T*>(a.v) + (k0 + j) * a.v_stride + hk * D + lane * E;
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += qv[e] * dev::to_f32(k[e]);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(m, s), c = exp2f(m - mn), p = exp2f(s - mn);
-    m = mn;
-    l = l * c + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * dev::to_f32(v[e]);
-  }
-  T* out = static_cast<T*>(a.out) + row * a.out_stride + h * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = dev::from_f32<T>(end <= 0 ? 0.0f : o[e] / l);
+  n = q1 - q0;
+  m = k1 - k0;
 }
 
-template <typename T>
-cudaError_t prefill_t(const PrefillArgs& a, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((a.total_q + kWarps - 1) / kWarps), static_cast<unsigned>(a.heads));
-  const float c = a.scale * 1.4426950408889634f;
-  if (a.head_dim == 64)
-    attn_prefill_kernel<T, 64><<<grid, kWarps * 32, 0, stream>>>(a, c);
-  else
-    attn_prefill_kernel<T, 128><<<grid, kWarps * 32, 0, stream>>>(a, c);
-  return cudaGetLastError();
+// The item's sequence, tile and heads; the whole warp calls.  false: there is
+// no such item.
+__device__ __forceinline__ bool find_item(const Args& a, int x, int lane, Item& it) {
+  const int rows = a.two_heads ? kTile : 2 * kTile;
+  int before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    int q0 = 0, n = 0, k0 = 0, m = 0;
+    if (b0 + lane < a.B) sequence(a, b0 + lane, q0, n, k0, m);
+    const int tiles = (n + rows - 1) / rows;
+    int incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    const int at = x / a.pairs - before;
+    const unsigned hit = __ballot_sync(0xffffffffu, incl > at);
+    if (hit != 0) {
+      const int src = __ffs(hit) - 1;
+      it.q0 = __shfl_sync(0xffffffffu, q0, src);
+      it.n = __shfl_sync(0xffffffffu, n, src);
+      it.k0 = __shfl_sync(0xffffffffu, k0, src);
+      it.m = __shfl_sync(0xffffffffu, m, src);
+      // the sequence's later tiles first
+      const int tile = __shfl_sync(0xffffffffu, incl, src) - 1 - at;
+      const int pair = x % a.pairs;
+      it.clean_from = INT_MAX;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        it.row[s] = a.two_heads ? tile * kTile : (2 * tile + s) * kTile;
+        it.head[s] = a.two_heads ? 2 * pair + s : pair;
+        it.on[s] = it.row[s] < it.n;
+        const int last_row = min(it.row[s] + kTile, it.n) - 1;
+        it.blocks[s] = it.on[s] ? (max(0, it.limit(last_row, a.causal)) + kTile - 1) / kTile : 0;
+        if (it.blocks[s] > 0) it.clean_from = min(it.clean_from, max(0, it.limit(it.row[s], a.causal)));
+      }
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::f16.
+__device__ __forceinline__ void mma_f16_ss(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Descriptor of a right operand stored with its columns contiguous (MN-major,
+// V as it lies): 64 columns in a 128-byte swizzled row, 8-row groups 1024
+// bytes apart (stride offset), the next 64 columns a sub-tile further on
+// (leading offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t sub_bytes) {
+  uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(sub_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+// Wait for this thread's tensor-memory loads; the values pass through, so
+// that nothing that uses them moves in front of the wait.
+__device__ __forceinline__ void wait_ld_32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                 "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                 "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// (v0 + n) * c, (v1 + n) * c.  The difference comes first: it is exact where
+// scores are near their maximum, however large they are.
+__device__ __forceinline__ float2 shift_scale2(uint32_t v0, uint32_t v1, float n, float c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tadd.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 y, {%5, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(v0), "r"(v1), "f"(n), "f"(c));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return dev::h2_bits(__floats2half2_rn(lo, hi));
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                    const __grid_constant__ CUtensorMap v_map, const Args a) {
+  using C = Cfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  unsigned char* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
+  const uint32_t base = ptx::smem_addr(smem);
+  auto bar = [&](int i) { return base + C::kOffBars + 8u * i; };
+  auto kv_full = [&](int s) { return bar(s); };
+  auto kv_empty = [&](int s) { return bar(C::kStages + s); };
+  const uint32_t q_full = bar(2 * C::kStages), q_empty = bar(2 * C::kStages + 1);
+  auto s_full = [&](int s) { return bar(2 * C::kStages + 2 + s); };
+  auto p_full = [&](int s) { return bar(2 * C::kStages + 4 + s); };
+  auto o_full = [&](int s) { return bar(2 * C::kStages + 6 + s); };
+  auto v_raw = [&](int i) { return bar(2 * C::kStages + 8 + i % kRaw); };
+  const uint32_t mma_done = bar(2 * C::kStages + 8 + kRaw);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  volatile int* found = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(kv_full(s), 2);      // the loader twice, or each cleaning warp
+      ptx::mbar_init(kv_empty(s), 1);
+    }
+    ptx::mbar_init(q_full, 1);
+    ptx::mbar_init(q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(s_full(s), 1);
+      ptx::mbar_init(p_full(s), 4);
+      ptx::mbar_init(o_full(s), 1);
+    }
+    for (int i = 0; i < kRaw; ++i) ptx::mbar_init(v_raw(i), 1);
+    ptx::mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tensormap(&q_map);
+    ptx::prefetch_tensormap(&k_map);
+    ptx::prefetch_tensormap(&v_map);
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(ptx::smem_addr(tmem_holder), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  auto fail = [&]() {
+    *abort_flag = 1;
+    atomicOr(&g_attn_prefill_error_flags, 1u);
+  };
+  // The whole warp waits, one lane acts (see the prefill GEMM).
+  auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(b, parity))) return true;
+    const bool got = ptx::mbar_wait_bounded(b, parity, abort_flag, kWaitLimitNs);
+    if (__all_sync(0xffffffffu, got)) return true;
+    fail();
+    return false;
+  };
+  // tensor memory: S (and P) of tile s at 128 s, O at 256 + 128 s
+  const int G = gridDim.x;
+
+  if (warp == kLoadWarp) {
+    // --------------------------------- copies ---------------------------------
+    int g = 0;                 // K and V blocks issued
+    int raws = 0;              // V blocks to be cleaned
+    bool ok = true;
+    Item it;
+    // a V block to be cleaned is announced to the warps that do it, which
+    // announce it as full
+    auto block = [&](const CUtensorMap* map, int col, int row, bool clean) {
+      const int s = g % C::kStages;
+      if (!warp_wait(kv_empty(s), ((g / C::kStages) & 1) ^ 1)) return false;
+      if (lane == 0) {
+        const uint32_t b = clean ? v_raw(raws) : kv_full(s);
+        ptx::mbar_arrive_expect_tx(b, C::kBlock);
+        if (!clean) ptx::mbar_arrive(b);
+        for (int i = 0; i < C::kSubs; ++i)
+          ptx::tma_load_2d(base + C::kOffRing + s * C::kBlock + i * C::kSub, map, col + 64 * i, row, b);
+      }
+      __syncwarp();
+      ++g;
+      raws += clean;
+      return true;
+    };
+    int items = 0;
+    for (int x = blockIdx.x; ok && x < a.max_items && find_item(a, x, lane, it); x += G) {
+      if (it.last() == 0) continue;
+      ok = warp_wait(q_empty, (items & 1) ^ 1);
+      if (!ok) break;
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(q_full, (it.blocks[0] > 0 ? C::kBlock : 0) + (it.blocks[1] > 0 ? C::kBlock : 0));
+        for (int s = 0; s < 2; ++s)
+          if (it.blocks[s] > 0)
+            for (int i = 0; i < C::kSubs; ++i)
+              ptx::tma_load_2d(base + s * C::kBlock + i * C::kSub, &q_map, it.head[s] * D + 64 * i, it.q0 + it.row[s], q_full);
+      }
+      __syncwarp();
+      ++items;
+      const int col = it.head[0] / a.group * D;
+      for (int j = 0; ok && j < it.last(); ++j)
+        ok = block(&k_map, col, it.k0 + j * kTile, false) &&
+             block(&v_map, col, it.k0 + j * kTile, (j + 1) * kTile > it.clean_from);
+    }
+    if (*abort_flag) {
+      // the MMAs may have stopped: wait for the copies in flight
+      if (items > 0) ptx::mbar_wait_bounded(q_full, (items - 1) & 1, nullptr, kWaitLimitNs);
+      for (int i = max(0, raws - kRaw); i < raws; ++i)
+        ptx::mbar_wait_bounded(v_raw(i), (i / kRaw) & 1, nullptr, kWaitLimitNs);
+      for (int i = max(0, g - C::kStages); i < g; ++i)
+        ptx::mbar_wait_bounded(kv_full(i % C::kStages), (i / C::kStages) & 1, nullptr, kWaitLimitNs / 16);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------- MMAs ----------------------------------
+    constexpr uint32_t kFmt = BF16 ? (1u << 7) | (1u << 10) : 0u;
+    constexpr uint32_t idesc_s = ptx::idesc_f16_f32(kTile, kTile) | kFmt;
+    constexpr uint32_t idesc_o = ptx::idesc_f16_f32(kTile, D) | kFmt | (1u << 16);   // V: columns contiguous
+    int g = 0, items = 0;
+    int p_count[2] = {0, 0};
+    bool ok = true;
+    Item it;
+    auto ring = [&](int i) { return base + C::kOffRing + (i % C::kStages) * C::kBlock; };
+    auto wait_block = [&](int i) { return warp_wait(kv_full(i % C::kStages), (i / C::kStages) & 1); };
+    auto scores = [&](int s, int kblock) {       // lane 0
+      const uint64_t q = ptx::sw128_kmajor_desc(base + s * C::kBlock), k = ptx::sw128_kmajor_desc(ring(kblock));
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t off = ((i / 4) * C::kSub + (i % 4) * 32) >> 4;
+        mma_f16_ss(tmem + 128 * s, q + off, k + off, idesc_s, i > 0);
+      }
+      ptx::mma_commit(s_full(s));
+    };
+    auto values = [&](int s, int vblock, bool first) {
+      const uint64_t v = sw128_mnmajor_desc(ring(vblock), C::kSub);
+#pragma unroll
+      for (int i = 0; i < kTile / 16; ++i)
+        ptx::mma_f16_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * i, v + ((i * 16 * 128) >> 4), idesc_o, !first || i > 0);
+    };
+    for (int x = blockIdx.x; ok && x < a.max_items && find_item(a, x, lane, it); x += G) {
+      const int N = it.last();
+      if (N == 0) continue;
+      ok = warp_wait(q_full, items & 1) && wait_block(g);
+      if (!ok) break;
+      if (lane == 0) {
+        ptx::tc_fence_after();
+        for (int s = 0; s < 2; ++s)
+          if (it.blocks[s] > 0) scores(s, g);
+        ptx::mma_commit(kv_empty(g % C::kStages));
+        if (N == 1) ptx::mma_commit(q_empty);
+      }
+      __syncwarp();
+      ++items;
+      for (int j = 0; ok && j < N; ++j) {
+        const int v = g + 2 * j + 1, k = v + 1;       // ring places of V_j and K_j+1
+        ok = wait_block(v) && (j + 1 == N || wait_block(k));
+        for (int s = 0; ok && s < 2; ++s) {
+          if (j >= it.blocks[s]) continue;
+          ok = warp_wait(p_full(s), p_count[s]++ & 1);
+          if (ok && lane == 0) {
+            ptx::tc_fence_after();
+            values(s, v, j == 0);
+            if (j + 1 < it.blocks[s])
+              scores(s, k);
+            else
+              ptx::mma_commit(o_full(s));
+          }
+          __syncwarp();
+        }
+        if (ok && lane == 0) {
+          ptx::mma_commit(kv_empty(v % C::kStages));
+          if (j + 1 < N) ptx::mma_commit(kv_empty(k % C::kStages));
+          if (j + 2 == N) ptx::mma_commit(q_empty);
+        }
+        __syncwarp();
+      }
+      g += 2 * N;
+    }
+    // no MMA may still use shared or tensor memory when they are released
+    if (lane == 0) ptx::mma_commit(mma_done);
+    __syncwarp();
+    ptx::mbar_wait_bounded(mma_done, 0, nullptr, kWaitLimitNs);
+  } else if (warp >= kFixWarp) {
+    // ------------------------ V blocks with unseen keys ------------------------
+    volatile int* my_found = found + (warp - kFixWarp) * kItemFlags;
+    int g = 0, items = 0, raws = 0;
+    bool ok = true;
+    Item it;
+    for (int x = blockIdx.x; ok && x < a.max_items && find_item(a, x, lane, it); x += G) {
+      const int N = it.last();
+      if (N == 0) continue;
+      // each warp has its own flags; those of an item kItemFlags behind are
+      // no longer read, the ring being shorter than that
+      if (lane == 0) my_found[items % kItemFlags] = 0;
+      __syncwarp();
+      for (int j = 0; ok && j < N; ++j) {
+        if ((j + 1) * kTile <= it.clean_from) continue;
+        const int v = g + 2 * j + 1;
+        ok = warp_wait(v_raw(raws), (raws / kRaw) & 1);
+        ++raws;
+        if (!ok) break;
+        unsigned char* tile = smem + C::kOffRing + (v % C::kStages) * C::kBlock;
+        const int end = it.m - j * kTile;      // rows from here on are not the sequence's
+        bool any = false;
+        // eight lanes a row of 128 bytes; the swizzle only permutes them
+        for (int r = max(0, it.clean_from - j * kTile) + (warp - kFixWarp) * 4 + (lane >> 3); r < kTile; r += 8) {
+#pragma unroll
+          for (int i = 0; i < C::kSubs; ++i) {
+            uint4* p = reinterpret_cast<uint4*>(tile + i * C::kSub + r * 128) + (lane & 7);
+            if (r >= end) {
+              *p = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            // exponent all ones: NaN or infinity
+            constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
+            uint4 w = *p;
+            uint32_t* u = &w.x;
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t hit = ((u[e] & kExp) + kOne) & 0x80008000u;
+              if (hit != 0) {
+                bad = true;
+                if (hit & 0x8000u) u[e] &= 0xFFFF0000u;
+                if (hit & 0x80000000u) u[e] &= 0x0000FFFFu;
+              }
+            }
+            if (bad) *p = w;
+            any |= bad;
+          }
+        }
+        if (any) my_found[items % kItemFlags] = 1;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(kv_full(v % C::kStages));
+      }
+      g += 2 * N;
+      ++items;
+    }
+  } else {
+    // --------------------------------- softmax ---------------------------------
+    const int s = warp >> 2;                       // tile
+    const int r = threadIdx.x & 127;               // row of the tile
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + 128 * s, t_o = tmem + lanes + 256 + 128 * s;
+    const float c = a.scale_log2;
+    int count = 0, o_count = 0, items = 0;
+    bool ok = true;
+    Item it;
+    for (int x = blockIdx.x; ok && x < a.max_items && find_item(a, x, lane, it); x += G) {
+      const bool counted = it.last() > 0;
+      const int item = items;
+      if (counted) ++items;
+      if (!it.on[s]) continue;
+      const int row = it.row[s] + r;               // query of the sequence
+      const int limit = it.limit(row, a.causal);
+      float ref = 0.0f, l = 0.0f;                  // reference (a score); sum
+      bool none = true;                            // no reference yet
+      for (int j = 0; ok && j < it.blocks[s]; ++j) {
+        ok = warp_wait(s_full(s), count++ & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const int seen = limit - j * kTile;        // keys of the block that the row sees
+        const bool masked = __any_sync(0xffffffffu, seen < kTile);
+        uint32_t p[64];
+        // One pass: the exponentials against the reference, their sum, and
+        // the block's maximum.  Returns the sum.
+        float top;
+        auto pass = [&](bool exps) -> float {
+          float sum0 = 0.0f, sum1 = 0.0f;
+          top = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t v[32];
+            ptx::tmem_ld_32cols(t_s + 32 * q, v);
+            wait_ld_32(v);
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (32 * q + i >= seen) v[i] = 0xFF800000u;       // -infinity
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+            if (exps) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 t = shift_scale2(v[i], v[i + 1], -ref, c);
+                const float e0 = exp2_approx(t.x), e1 = exp2_approx(t.y);
+                sum0 += e0;
+                sum1 += e1;
+                p[16 * q + i / 2] = pack2<BF16>(e0, e1);
+              }
+            }
+          }
+          return sum0 + sum1;
+        };
+        float sum = 0.0f;
+        const bool fresh = __any_sync(0xffffffffu, none);
+        if (!fresh) sum = pass(true);
+        bool grow = none;
+        if (!fresh) grow = (top - ref) * c > kLazy;
+        if (fresh || __any_sync(0xffffffffu, grow)) {
+          // a new reference for the rows that passed theirs (or have none)
+          if (fresh) {
+            pass(false);
+            grow = none ? top > -INFINITY : (top - ref) * c > kLazy;
+          }
+          const float mn = grow ? top : ref;
+          const float f = none ? 0.0f : exp2_approx((ref - mn) * c);
+          if (grow) {
+            l *= f;
+            none = false;
+          }
+          ref = mn;
+          if (j > 0 && __any_sync(0xffffffffu, grow)) {
+            // O of the blocks so far: their product finished before this S
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t v[32];
+              ptx::tmem_ld_32cols(t_o + 32 * q, v);
+              wait_ld_32(v);
+              const float ff = grow ? f : 1.0f;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * ff);
+              ptx::tmem_st_32cols(t_o + 32 * q, v);
+            }
+          }
+          sum = pass(true);
+        }
+        l += sum;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = p[32 * q + i];
+          ptx::tmem_st_32cols(t_s + 32 * q, v);
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(p_full(s));
+      }
+      if (!ok) break;
+      // -------- the tile's results
+      const bool some = it.blocks[s] > 0;
+      if (some) {
+        ok = warp_wait(o_full(s), o_count++ & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+      }
+      const float inv = l > 0.0f ? __fdividef(1.0f, l) : l;       // nothing seen: 0; NaN stays
+      const bool patch = counted && (found[item % kItemFlags] | found[kItemFlags + item % kItemFlags]) != 0;
+      using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+      T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(it.q0) + row) * a.out_stride + it.head[s] * D;
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t v[32];
+        if (some) {
+          ptx::tmem_ld_32cols(t_o + 32 * q, v);
+          wait_ld_32(v);
+        }
+        float e[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) e[i] = some && l != 0.0f ? __uint_as_float(v[i]) * inv : 0.0f;
+        if (patch) {
+          // the NaN and infinities that this row sees among the cleaned keys
+          for (int k = it.clean_from; k < limit; ++k) {
+            const T* src = static_cast<const T*>(a.v) + (static_cast<int64_t>(it.k0) + k) * a.v_stride +
+                           it.head[s] / a.group * D + 32 * q;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float f = dev::to_f32(src[i]);
+              if (!(fabsf(f) <= 3.4e38f)) e[i] += f;
+            }
+          }
+        }
+        if (row < it.n) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(out + 32 * q + i) =
+                make_uint4(pack2<BF16>(e[i], e[i + 1]), pack2<BF16>(e[i + 2], e[i + 3]),
+                           pack2<BF16>(e[i + 4], e[i + 5]), pack2<BF16>(e[i + 6], e[i + 7]));
+        }
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// Packed rows as [rows][width] 16-bit elements, boxes of 64 columns and 128 rows.
+bool row_map(CUtensorMap* map, const void* p, int64_t rows, int64_t width, int64_t stride, bool bf16) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[2] = {64, kTile};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool BF16>
+cudaError_t prefill_t(const PrefillArgs& p, cudaStream_t stream) {
+  using C = Cfg<D>;
+  CUtensorMap q_map, k_map, v_map;
+  const bool keys = p.total_k > 0;      // without any, no key is loaded
+  if (!row_map(&q_map, p.q, p.total_q, p.heads * D, p.q_stride, BF16) ||
+      !row_map(&k_map, keys ? p.k : p.q, keys ? p.total_k : 1, keys ? p.kv_heads * D : D, keys ? p.k_stride : D, BF16) ||
+      !row_map(&v_map, keys ? p.v : p.q, keys ? p.total_k : 1, keys ? p.kv_heads * D : D, keys ? p.v_stride : D, BF16))
+    return cudaErrorInvalidValue;
+  static SmemAttrOnce attr;
+  cudaError_t e = attr.ensure(attn_prefill_kernel<D, BF16>, C::kSmem);
+  if (e != cudaSuccess) return e;
+  Args a = {};
+  a.v = p.v;
+  a.out = p.out;
+  a.v_stride = p.v_stride;
+  a.out_stride = p.out_stride;
+  a.cu_q = p.cu_q;
+  a.cu_k = p.cu_k;
+  a.B = static_cast<int>(p.B);
+  a.total_q = static_cast<int>(p.total_q);
+  a.total_k = static_cast<int>(p.total_k);
+  a.heads = static_cast<int>(p.heads);
+  a.group = static_cast<int>(p.heads / p.kv_heads);
+  a.two_heads = a.group % 2 == 0;
+  a.pairs = a.two_heads ? a.heads / 2 : a.heads;
+  a.scale_log2 = p.scale * 1.4426950408889634f;
+  a.causal = p.causal != 0;
+  // at most one ragged tile per sequence
+  const int64_t rows = a.two_heads ? kTile : 2 * kTile;
+  const int64_t items = (p.total_q / rows + p.B) * a.pairs;
+  if (items > INT32_MAX / 2) return cudaErrorInvalidValue;
+  a.max_items = static_cast<int>(items);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(device_sm_count(), items)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute pdl;
+  pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D, BF16>, q_map, k_map, v_map, a);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_prefill(const PrefillArgs& a, int dtype, cudaStream_t stream) {
-  return dtype == NVQ_F16 ? prefill_t<__half>(a, stream) : prefill_t<__nv_bfloat16>(a, stream);
+  if (a.head_dim == 64)
+    return dtype == NVQ_F16 ? prefill_t<64, false>(a, stream) : prefill_t<64, true>(a, stream);
+  return dtype == NVQ_F16 ? prefill_t<128, false>(a, stream) : prefill_t<128, true>(a, stream);
 }
 
 cudaError_t attn_prefill_error_flags(bool clear, unsigned int* flags) {
