@@ -58,6 +58,7 @@ constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr float kLazy = 8.0f;
+constexpr int kPolyOf4 = 1;           // quarters of the exponentials formed without the special-function units
 constexpr int kItemFlags = 8;        // found flags of the last items
 constexpr int kRaw = 4;              // V blocks on their way to be cleaned (the ring holds fewer)
 
@@ -196,15 +197,67 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// (v0 + n) * c, (v1 + n) * c.  The difference comes first: it is exact where
-// scores are near their maximum, however large they are.
-__device__ __forceinline__ float2 shift_scale2(uint32_t v0, uint32_t v1, float n, float c) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tadd.rn.f32x2 x, x, y;\n\t"
-      "mov.b64 y, {%5, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "r"(v0), "r"(v1), "f"(n), "f"(c));
+// Wait for 16 columns, as above.
+__device__ __forceinline__ void wait_ld_16(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+// Pairs of fp32 values in one instruction.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
   return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ float2 split2(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// The largest of three; NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 2^x by multiplications and additions, for a part of the exponentials, so
+// that the special-function units are not the only ones at work: x = n + f
+// with n the nearest whole number (the rounding of a large addend leaves it in
+// the low bits), 2^f = 1 + f q(f) on [-1/2, 1/2], q of degree 3 fitted for the
+// least largest relative error (2.9e-6, far below the rounding of P to 16
+// bits), n added to the exponent.  Exact at 0.  x below -126 gives 2^-126; NaN
+// and infinities are left to the caller.
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+  const F2 kRound = f2(12582912.0f);     // 1.5 * 2^23
+  const F2 v = f2(fmaxf(x.x, -126.0f), fmaxf(x.y, -126.0f));
+  const F2 t = add2(v, kRound);
+  const F2 f = add2(v, mul2(add2(t, f2(-12582912.0f)), f2(-1.0f)));
+  F2 y = fma2(f2(0x1.3a02ccp-7f), f, f2(0x1.c9fc46p-5f));
+  y = fma2(y, f, f2(0x1.ec0378p-3f));
+  y = fma2(y, f, f2(0x1.62e12cp-1f));
+  y = fma2(y, f, f2(1.0f));
+  const float2 n = split2(t), m = split2(y);
+  return make_float2(__uint_as_float(__float_as_uint(m.x) + (__float_as_uint(n.x) << 23)),
+                     __uint_as_float(__float_as_uint(m.y) + (__float_as_uint(n.y) << 23)));
 }
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -487,45 +540,62 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         const bool masked = __any_sync(0xffffffffu, seen < kTile);
         uint32_t p[64];
         // One pass: the exponentials against the reference, their sum, and
-        // the block's maximum.  Returns the sum.
+        // the block's maximum (NaN if a score is).  Returns the sum.
         float top;
-        auto pass = [&](bool exps) -> float {
-          float sum0 = 0.0f, sum1 = 0.0f;
+        auto pass = [&](auto exps) -> float {
+          F2 sum0 = f2(0.0f), sum1 = f2(0.0f);
+          const F2 n2 = f2(-ref), c2 = f2(c);
           top = -INFINITY;
+          uint32_t v[2][16];
+          ptx::tmem_ld_16cols(t_s, v[0]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t v[32];
-            ptx::tmem_ld_32cols(t_s + 32 * q, v);
-            wait_ld_32(v);
+          for (int q = 0; q < 8; ++q) {
+            uint32_t(&w)[16] = v[q & 1];
+            wait_ld_16(w);
+            if (q < 7) ptx::tmem_ld_16cols(t_s + 16 * (q + 1), v[(q + 1) & 1]);
             if (masked) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (32 * q + i >= seen) v[i] = 0xFF800000u;       // -infinity
+              for (int i = 0; i < 16; ++i)
+                if (16 * q + i >= seen) w[i] = 0xFF800000u;       // -infinity
             }
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
-            if (exps) {
+            for (int i = 0; i < 16; i += 2) top = max3_nan(top, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+            if constexpr (decltype(exps)::value) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 t = shift_scale2(v[i], v[i + 1], -ref, c);
-                const float e0 = exp2_approx(t.x), e1 = exp2_approx(t.y);
-                sum0 += e0;
-                sum1 += e1;
-                p[16 * q + i / 2] = pack2<BF16>(e0, e1);
+              for (int i = 0; i < 16; i += 2) {
+                // the difference comes first: it is exact where scores are
+                // near their maximum, however large they are
+                const float2 t = split2(mul2(add2(f2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), n2), c2));
+                float2 e;
+                if (i / 2 % 4 < kPolyOf4) {
+                  e = exp2_poly(t);
+                  if (masked) {
+                    if (16 * q + i >= seen) e.x = 0.0f;
+                    if (16 * q + i + 1 >= seen) e.y = 0.0f;
+                  }
+                } else {
+                  e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
+                }
+                (i & 2 ? sum1 : sum0) = add2(i & 2 ? sum1 : sum0, f2(e.x, e.y));
+                p[8 * q + i / 2] = pack2<BF16>(e.x, e.y);
               }
             }
           }
-          return sum0 + sum1;
+          const float2 total = split2(add2(sum0, sum1));
+          // a score that is NaN or +infinity makes the row NaN
+          return top < INFINITY ? total.x + total.y : __int_as_float(0x7FFFFFFF);
         };
+        using Exps = std::integral_constant<bool, true>;
+        using MaxOnly = std::integral_constant<bool, false>;
         float sum = 0.0f;
         const bool fresh = __any_sync(0xffffffffu, none);
-        if (!fresh) sum = pass(true);
+        if (!fresh) sum = pass(Exps{});
         bool grow = none;
         if (!fresh) grow = (top - ref) * c > kLazy;
         if (fresh || __any_sync(0xffffffffu, grow)) {
           // a new reference for the rows that passed theirs (or have none)
           if (fresh) {
-            pass(false);
+            pass(MaxOnly{});
             grow = none ? top > -INFINITY : (top - ref) * c > kLazy;
           }
           const float mn = grow ? top : ref;
@@ -548,7 +618,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
               ptx::tmem_st_32cols(t_o + 32 * q, v);
             }
           }
-          sum = pass(true);
+          sum = pass(Exps{});
         }
         l += sum;
 #pragma unroll
