@@ -19,7 +19,6 @@
 //   warp 8      issues the MMAs: per key block and tile O += P V, then the next
 //               S (a tile's S and P share their columns, so in this order)
 //   warp 9      TMA: both Q tiles, then K and V blocks into a ring
-//   warps 10-11 clean a V block that some query does not see all of (below)
 //
 // The two tiles share K and V: two heads of one key-value head with the same
 // 128 queries where the group is even, else 256 queries of one head.  Work
@@ -32,10 +31,11 @@
 // formed after it) and forms the block again.
 //
 // A key behind a query's last one gets p = 0, but 0 * NaN is not 0: before a
-// block with such keys is used, rows of V behind the sequence's end are
-// zeroed in shared memory, and NaN and infinities in rows that only some of
-// the queries see are replaced by 0 and added to those queries' results at
-// the end.
+// block with such keys is used, the softmax warps zero the rows of V behind
+// the sequence's end in shared memory, and replace NaN and infinities in rows
+// that only some of the queries see by 0 and add them to those queries'
+// results at the end.  Both tiles' warps do all of it (the second finds it
+// done), as either may be the first to release its product.
 #include <algorithm>
 #include <climits>
 #include <mutex>
@@ -54,13 +54,11 @@ namespace nvq {
 namespace {
 
 constexpr int kTile = 128;           // queries of a tile, keys of a block
-constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kFixWarp = 10;
+constexpr int kThreads = 320;        // 10 warps: 200 registers a thread
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr float kLazy = 8.0f;
-constexpr int kPolyOf4 = 1;           // quarters of the exponentials formed without the special-function units
 constexpr int kItemFlags = 8;        // found flags of the last items
-constexpr int kRaw = 4;              // V blocks on their way to be cleaned (the ring holds fewer)
 
 __device__ unsigned int g_attn_prefill_error_flags = 0;   // bit 0: a wait timed out, bit 1: a bad index
 
@@ -72,9 +70,9 @@ struct Cfg {
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kOffRing = 2 * kBlock;
   static constexpr int kOffBars = kOffRing + kStages * kBlock;
-  static constexpr int kBars = 2 * kStages + 2 + 6 + kRaw + 1;
+  static constexpr int kBars = 2 * kStages + 2 + 6 + 1;
   static constexpr int kOffMisc = kOffBars + 8 * kBars;
-  static constexpr int kSmem = kOffMisc + 16 + 8 * kItemFlags + 1024;
+  static constexpr int kSmem = kOffMisc + 16 + 4 * kItemFlags + 1024;
 };
 
 struct Args {
@@ -197,14 +195,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Wait for 16 columns, as above.
-__device__ __forceinline__ void wait_ld_16(uint32_t (&v)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-               :
-               : "memory");
-}
 // Pairs of fp32 values in one instruction.
 using F2 = unsigned long long;
 __device__ __forceinline__ F2 f2(float x, float y) {
@@ -228,36 +218,11 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 // The largest of three; NaN if one is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-// 2^x by multiplications and additions, for a part of the exponentials, so
-// that the special-function units are not the only ones at work: x = n + f
-// with n the nearest whole number (the rounding of a large addend leaves it in
-// the low bits), 2^f = 1 + f q(f) on [-1/2, 1/2], q of degree 3 fitted for the
-// least largest relative error (2.9e-6, far below the rounding of P to 16
-// bits), n added to the exponent.  Exact at 0.  x below -126 gives 2^-126; NaN
-// and infinities are left to the caller.
-__device__ __forceinline__ float2 exp2_poly(float2 x) {
-  const F2 kRound = f2(12582912.0f);     // 1.5 * 2^23
-  const F2 v = f2(fmaxf(x.x, -126.0f), fmaxf(x.y, -126.0f));
-  const F2 t = add2(v, kRound);
-  const F2 f = add2(v, mul2(add2(t, f2(-12582912.0f)), f2(-1.0f)));
-  F2 y = fma2(f2(0x1.3a02ccp-7f), f, f2(0x1.c9fc46p-5f));
-  y = fma2(y, f, f2(0x1.ec0378p-3f));
-  y = fma2(y, f, f2(0x1.62e12cp-1f));
-  y = fma2(y, f, f2(1.0f));
-  const float2 n = split2(t), m = split2(y);
-  return make_float2(__uint_as_float(__float_as_uint(m.x) + (__float_as_uint(n.x) << 23)),
-                     __uint_as_float(__float_as_uint(m.y) + (__float_as_uint(n.y) << 23)));
 }
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -266,6 +231,46 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
   }
   return dev::h2_bits(__floats2half2_rn(lo, hi));
+}
+
+// 128 threads (thread r of them): rows `from`.. of a V block in shared memory:
+// those from `end` on are set to zero, in the others NaN and infinities.
+// *found is set before one is taken out, so whoever finds it gone finds the flag
+// set too.  Eight lanes take a row of 128 bytes; the swizzle only permutes it.
+// Nothing is written where nothing changes, since the other tile's product
+// may be reading a block that is clean.
+template <int SUBS, bool BF16>
+__device__ __noinline__ void clean_values(unsigned char* block, int sub_bytes, int from, int end, int r,
+                                          volatile int* found) {
+  constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
+  for (int row = from + (r >> 3); row < kTile; row += 16) {
+#pragma unroll
+    for (int i = 0; i < SUBS; ++i) {
+      uint4* p = reinterpret_cast<uint4*>(block + i * sub_bytes + row * 128) + (r & 7);
+      uint4 w = *p;
+      if (row >= end) {
+        if ((w.x | w.y | w.z | w.w) != 0) *p = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      uint32_t* u = &w.x;
+      bool bad = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t hit = ((u[e] & kExp) + kOne) & 0x80008000u;   // exponent all ones
+        if (hit != 0) {
+          bad = true;
+          if (hit & 0x8000u) u[e] &= 0xFFFF0000u;
+          if (hit & 0x80000000u) u[e] &= 0x0000FFFFu;
+        }
+      }
+      if (bad) {
+        *found = 1;
+        __threadfence_block();
+        *p = w;
+      }
+    }
+  }
+  __threadfence_block();
 }
 
 template <int D, bool BF16>
@@ -284,8 +289,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   auto s_full = [&](int s) { return bar(2 * C::kStages + 2 + s); };
   auto p_full = [&](int s) { return bar(2 * C::kStages + 4 + s); };
   auto o_full = [&](int s) { return bar(2 * C::kStages + 6 + s); };
-  auto v_raw = [&](int i) { return bar(2 * C::kStages + 8 + i % kRaw); };
-  const uint32_t mma_done = bar(2 * C::kStages + 8 + kRaw);
+  const uint32_t mma_done = bar(2 * C::kStages + 8);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* found = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);
@@ -293,7 +297,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      ptx::mbar_init(kv_full(s), 2);      // the loader twice, or each cleaning warp
+      ptx::mbar_init(kv_full(s), 1);
       ptx::mbar_init(kv_empty(s), 1);
     }
     ptx::mbar_init(q_full, 1);
@@ -303,9 +307,9 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       ptx::mbar_init(p_full(s), 4);
       ptx::mbar_init(o_full(s), 1);
     }
-    for (int i = 0; i < kRaw; ++i) ptx::mbar_init(v_raw(i), 1);
     ptx::mbar_init(mma_done, 1);
     *abort_flag = 0;
+    for (int i = 0; i < kItemFlags; ++i) found[i] = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tensormap(&q_map);
     ptx::prefetch_tensormap(&k_map);
@@ -340,24 +344,18 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   if (warp == kLoadWarp) {
     // --------------------------------- copies ---------------------------------
     int g = 0;                 // K and V blocks issued
-    int raws = 0;              // V blocks to be cleaned
     bool ok = true;
     Item it;
-    // a V block to be cleaned is announced to the warps that do it, which
-    // announce it as full
-    auto block = [&](const CUtensorMap* map, int col, int row, bool clean) {
+    auto block = [&](const CUtensorMap* map, int col, int row) {
       const int s = g % C::kStages;
       if (!warp_wait(kv_empty(s), ((g / C::kStages) & 1) ^ 1)) return false;
       if (lane == 0) {
-        const uint32_t b = clean ? v_raw(raws) : kv_full(s);
-        ptx::mbar_arrive_expect_tx(b, C::kBlock);
-        if (!clean) ptx::mbar_arrive(b);
+        ptx::mbar_arrive_expect_tx(kv_full(s), C::kBlock);
         for (int i = 0; i < C::kSubs; ++i)
-          ptx::tma_load_2d(base + C::kOffRing + s * C::kBlock + i * C::kSub, map, col + 64 * i, row, b);
+          ptx::tma_load_2d(base + C::kOffRing + s * C::kBlock + i * C::kSub, map, col + 64 * i, row, kv_full(s));
       }
       __syncwarp();
       ++g;
-      raws += clean;
       return true;
     };
     int items = 0;
@@ -367,6 +365,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       if (!ok) break;
       if (lane == 0) {
         ptx::mbar_arrive_expect_tx(q_full, (it.blocks[0] > 0 ? C::kBlock : 0) + (it.blocks[1] > 0 ? C::kBlock : 0));
+#pragma unroll
         for (int s = 0; s < 2; ++s)
           if (it.blocks[s] > 0)
             for (int i = 0; i < C::kSubs; ++i)
@@ -376,16 +375,13 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       ++items;
       const int col = it.head[0] / a.group * D;
       for (int j = 0; ok && j < it.last(); ++j)
-        ok = block(&k_map, col, it.k0 + j * kTile, false) &&
-             block(&v_map, col, it.k0 + j * kTile, (j + 1) * kTile > it.clean_from);
+        ok = block(&k_map, col, it.k0 + j * kTile) && block(&v_map, col, it.k0 + j * kTile);
     }
     if (*abort_flag) {
       // the MMAs may have stopped: wait for the copies in flight
       if (items > 0) ptx::mbar_wait_bounded(q_full, (items - 1) & 1, nullptr, kWaitLimitNs);
-      for (int i = max(0, raws - kRaw); i < raws; ++i)
-        ptx::mbar_wait_bounded(v_raw(i), (i / kRaw) & 1, nullptr, kWaitLimitNs);
       for (int i = max(0, g - C::kStages); i < g; ++i)
-        ptx::mbar_wait_bounded(kv_full(i % C::kStages), (i / C::kStages) & 1, nullptr, kWaitLimitNs / 16);
+        ptx::mbar_wait_bounded(kv_full(i % C::kStages), (i / C::kStages) & 1, nullptr, kWaitLimitNs);
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------- MMAs ----------------------------------
@@ -419,7 +415,11 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       ok = warp_wait(q_full, items & 1) && wait_block(g);
       if (!ok) break;
       if (lane == 0) {
+        // the flag of an item to come: of those before this one only the last
+        // can still be read
+        found[(items + 2) % kItemFlags] = 0;
         ptx::tc_fence_after();
+#pragma unroll
         for (int s = 0; s < 2; ++s)
           if (it.blocks[s] > 0) scores(s, g);
         ptx::mma_commit(kv_empty(g % C::kStages));
@@ -430,8 +430,9 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       for (int j = 0; ok && j < N; ++j) {
         const int v = g + 2 * j + 1, k = v + 1;       // ring places of V_j and K_j+1
         ok = wait_block(v) && (j + 1 == N || wait_block(k));
-        for (int s = 0; ok && s < 2; ++s) {
-          if (j >= it.blocks[s]) continue;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (!ok || j >= it.blocks[s]) continue;
           ok = warp_wait(p_full(s), p_count[s]++ & 1);
           if (ok && lane == 0) {
             ptx::tc_fence_after();
@@ -456,63 +457,6 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
     if (lane == 0) ptx::mma_commit(mma_done);
     __syncwarp();
     ptx::mbar_wait_bounded(mma_done, 0, nullptr, kWaitLimitNs);
-  } else if (warp >= kFixWarp) {
-    // ------------------------ V blocks with unseen keys ------------------------
-    volatile int* my_found = found + (warp - kFixWarp) * kItemFlags;
-    int g = 0, items = 0, raws = 0;
-    bool ok = true;
-    Item it;
-    for (int x = blockIdx.x; ok && x < a.max_items && find_item(a, x, lane, it); x += G) {
-      const int N = it.last();
-      if (N == 0) continue;
-      // each warp has its own flags; those of an item kItemFlags behind are
-      // no longer read, the ring being shorter than that
-      if (lane == 0) my_found[items % kItemFlags] = 0;
-      __syncwarp();
-      for (int j = 0; ok && j < N; ++j) {
-        if ((j + 1) * kTile <= it.clean_from) continue;
-        const int v = g + 2 * j + 1;
-        ok = warp_wait(v_raw(raws), (raws / kRaw) & 1);
-        ++raws;
-        if (!ok) break;
-        unsigned char* tile = smem + C::kOffRing + (v % C::kStages) * C::kBlock;
-        const int end = it.m - j * kTile;      // rows from here on are not the sequence's
-        bool any = false;
-        // eight lanes a row of 128 bytes; the swizzle only permutes them
-        for (int r = max(0, it.clean_from - j * kTile) + (warp - kFixWarp) * 4 + (lane >> 3); r < kTile; r += 8) {
-#pragma unroll
-          for (int i = 0; i < C::kSubs; ++i) {
-            uint4* p = reinterpret_cast<uint4*>(tile + i * C::kSub + r * 128) + (lane & 7);
-            if (r >= end) {
-              *p = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            // exponent all ones: NaN or infinity
-            constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
-            uint4 w = *p;
-            uint32_t* u = &w.x;
-            bool bad = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t hit = ((u[e] & kExp) + kOne) & 0x80008000u;
-              if (hit != 0) {
-                bad = true;
-                if (hit & 0x8000u) u[e] &= 0xFFFF0000u;
-                if (hit & 0x80000000u) u[e] &= 0x0000FFFFu;
-              }
-            }
-            if (bad) *p = w;
-            any |= bad;
-          }
-        }
-        if (any) my_found[items % kItemFlags] = 1;
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(kv_full(v % C::kStages));
-      }
-      g += 2 * N;
-      ++items;
-    }
   } else {
     // --------------------------------- softmax ---------------------------------
     const int s = warp >> 2;                       // tile
@@ -520,19 +464,22 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + 128 * s, t_o = tmem + lanes + 256 + 128 * s;
     const float c = a.scale_log2;
-    int count = 0, o_count = 0, items = 0;
+    int g = 0, count = 0, o_count = 0, items = 0;
     bool ok = true;
     Item it;
     for (int x = blockIdx.x; ok && x < a.max_items && find_item(a, x, lane, it); x += G) {
       const bool counted = it.last() > 0;
       const int item = items;
+      const int g0 = g;                            // ring place of K_0
       if (counted) ++items;
-      if (!it.on[s]) continue;
-      const int row = it.row[s] + r;               // query of the sequence
+      g += 2 * it.last();
+      // this tile's values (selected, so that they stay in registers)
+      if (!(s ? it.on[1] : it.on[0])) continue;
+      const int row = (s ? it.row[1] : it.row[0]) + r;       // query of the sequence
+      const int blocks = s ? it.blocks[1] : it.blocks[0], head = s ? it.head[1] : it.head[0];
       const int limit = it.limit(row, a.causal);
       float ref = 0.0f, l = 0.0f;                  // reference (a score); sum
-      bool none = true;                            // no reference yet
-      for (int j = 0; ok && j < it.blocks[s]; ++j) {
+      for (int j = 0; ok && j < blocks; ++j) {
         ok = warp_wait(s_full(s), count++ & 1);
         if (!ok) break;
         ptx::tc_fence_after();
@@ -542,83 +489,77 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         // One pass: the exponentials against the reference, their sum, and
         // the block's maximum (NaN if a score is).  Returns the sum.
         float top;
-        auto pass = [&](auto exps) -> float {
+        auto hide = [&](uint32_t (&w)[32], int col) {
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (col + i >= seen) w[i] = 0xFF800000u;       // -infinity
+          }
+        };
+        auto pass = [&]() -> float {
           F2 sum0 = f2(0.0f), sum1 = f2(0.0f);
           const F2 n2 = f2(-ref), c2 = f2(c);
+          float top1 = -INFINITY;
           top = -INFINITY;
-          uint32_t v[2][16];
-          ptx::tmem_ld_16cols(t_s, v[0]);
+          uint32_t v[2][32];
+          ptx::tmem_ld_32cols(t_s, v[0]);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            uint32_t(&w)[16] = v[q & 1];
-            wait_ld_16(w);
-            if (q < 7) ptx::tmem_ld_16cols(t_s + 16 * (q + 1), v[(q + 1) & 1]);
-            if (masked) {
+          for (int q = 0; q < 4; ++q) {
+            uint32_t(&w)[32] = v[q & 1];
+            wait_ld_32(w);
+            if (q < 3) ptx::tmem_ld_32cols(t_s + 32 * (q + 1), v[(q + 1) & 1]);
+            hide(w, 32 * q);
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (16 * q + i >= seen) w[i] = 0xFF800000u;       // -infinity
+            for (int i = 0; i < 32; i += 4) {
+              top = max3_nan(top, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+              top1 = max3_nan(top1, __uint_as_float(w[i + 2]), __uint_as_float(w[i + 3]));
             }
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) top = max3_nan(top, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
-            if constexpr (decltype(exps)::value) {
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                // the difference comes first: it is exact where scores are
-                // near their maximum, however large they are
-                const float2 t = split2(mul2(add2(f2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), n2), c2));
-                float2 e;
-                if (i / 2 % 4 < kPolyOf4) {
-                  e = exp2_poly(t);
-                  if (masked) {
-                    if (16 * q + i >= seen) e.x = 0.0f;
-                    if (16 * q + i + 1 >= seen) e.y = 0.0f;
-                  }
-                } else {
-                  e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
-                }
-                (i & 2 ? sum1 : sum0) = add2(i & 2 ? sum1 : sum0, f2(e.x, e.y));
-                p[8 * q + i / 2] = pack2<BF16>(e.x, e.y);
-              }
+            for (int i = 0; i < 32; i += 2) {
+              // the difference comes first: it is exact where scores are
+              // near their maximum, however large they are
+              const float2 t = split2(mul2(add2(f2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), n2), c2));
+              const float2 e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
+              (i & 2 ? sum1 : sum0) = add2(i & 2 ? sum1 : sum0, f2(e.x, e.y));
+              p[16 * q + i / 2] = pack2<BF16>(e.x, e.y);
             }
           }
+          top = max3_nan(top, top1, top1);
           const float2 total = split2(add2(sum0, sum1));
           // a score that is NaN or +infinity makes the row NaN
           return top < INFINITY ? total.x + total.y : __int_as_float(0x7FFFFFFF);
         };
-        using Exps = std::integral_constant<bool, true>;
-        using MaxOnly = std::integral_constant<bool, false>;
-        float sum = 0.0f;
-        const bool fresh = __any_sync(0xffffffffu, none);
-        if (!fresh) sum = pass(Exps{});
-        bool grow = none;
-        if (!fresh) grow = (top - ref) * c > kLazy;
-        if (fresh || __any_sync(0xffffffffu, grow)) {
-          // a new reference for the rows that passed theirs (or have none)
-          if (fresh) {
-            pass(MaxOnly{});
-            grow = none ? top > -INFINITY : (top - ref) * c > kLazy;
-          }
-          const float mn = grow ? top : ref;
-          const float f = none ? 0.0f : exp2_approx((ref - mn) * c);
-          if (grow) {
-            l *= f;
-            none = false;
-          }
-          ref = mn;
-          if (j > 0 && __any_sync(0xffffffffu, grow)) {
+        if (j == 0) {
+          // the first reference: the largest of the first 32 scores
+          uint32_t w[32];
+          ptx::tmem_ld_32cols(t_s, w);
+          wait_ld_32(w);
+          hide(w, 0);
+          float first = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) first = max3_nan(first, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+          if (fabsf(first) < INFINITY) ref = first;
+        }
+        float sum = pass();
+        const bool grow = (top - ref) * c > kLazy;
+        if (__any_sync(0xffffffffu, grow)) {
+          // a new reference for the rows that passed theirs
+          const float f = grow ? exp2_approx((ref - top) * c) : 1.0f;
+          if (grow) ref = top;
+          l *= f;
+          if (j > 0) {
             // O of the blocks so far: their product finished before this S
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
               uint32_t v[32];
               ptx::tmem_ld_32cols(t_o + 32 * q, v);
               wait_ld_32(v);
-              const float ff = grow ? f : 1.0f;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * ff);
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
               ptx::tmem_st_32cols(t_o + 32 * q, v);
             }
           }
-          sum = pass(Exps{});
+          sum = pass();
         }
         l += sum;
 #pragma unroll
@@ -628,6 +569,17 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           for (int i = 0; i < 32; ++i) v[i] = p[32 * q + i];
           ptx::tmem_st_32cols(t_s + 32 * q, v);
         }
+        if ((j + 1) * kTile > it.clean_from) {
+          // V_j has keys that some query does not see (its place in the ring is
+          // this one until P is released)
+          const int v = g0 + 2 * j + 1;
+          ok = warp_wait(kv_full(v % C::kStages), (v / C::kStages) & 1);
+          if (!ok) break;
+          clean_values<C::kSubs, BF16>(smem + C::kOffRing + (v % C::kStages) * C::kBlock, C::kSub,
+                                       max(0, it.clean_from - j * kTile), it.m - j * kTile, r,
+                                       found + item % kItemFlags);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
@@ -635,16 +587,16 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       }
       if (!ok) break;
       // -------- the tile's results
-      const bool some = it.blocks[s] > 0;
+      const bool some = blocks > 0;
       if (some) {
         ok = warp_wait(o_full(s), o_count++ & 1);
         if (!ok) break;
         ptx::tc_fence_after();
       }
       const float inv = l > 0.0f ? __fdividef(1.0f, l) : l;       // nothing seen: 0; NaN stays
-      const bool patch = counted && (found[item % kItemFlags] | found[kItemFlags + item % kItemFlags]) != 0;
+      const bool patch = some && found[item % kItemFlags] != 0;
       using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-      T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(it.q0) + row) * a.out_stride + it.head[s] * D;
+      T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(it.q0) + row) * a.out_stride + head * D;
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
         uint32_t v[32];
@@ -659,7 +611,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           // the NaN and infinities that this row sees among the cleaned keys
           for (int k = it.clean_from; k < limit; ++k) {
             const T* src = static_cast<const T*>(a.v) + (static_cast<int64_t>(it.k0) + k) * a.v_stride +
-                           it.head[s] / a.group * D + 32 * q;
+                           head / a.group * D + 32 * q;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float f = dev::to_f32(src[i]);
