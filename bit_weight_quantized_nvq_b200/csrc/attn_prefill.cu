@@ -9,26 +9,28 @@
 // Two bounds are equally near at head_dim 128: a block of 128 queries and 128
 // keys takes the tensor core 2 x 512 cycles (S = Q K^T and O += P V) and the
 // special-function units 1024 cycles (16384 exponentials at 16 a cycle).  So
-// a persistent CTA per SM works on two query tiles at once, and while the
-// exponentials of one are formed the tensor core has the products of the other.
+// a persistent CTA per SM works on two query tiles at once, and each tile has
+// two S buffers of 64 keys: while the exponentials of one are formed the tensor
+// core has the other, and the other tile's.
 //
 //   warps 0-3   softmax of tile 0, one thread per query row: read S from
 //               tensor memory, write P = exp2(..) over it as the left operand
 //               of the next product; at the end O / sum -> out
 //   warps 4-7   the same for tile 1
-//   warp 8      issues the MMAs: per key block and tile O += P V, then the next
-//               S (a tile's S and P share their columns, so in this order)
-//   warp 9      TMA: both Q tiles, then K and V blocks into a ring
+//   warps 8, 9  issue the MMAs of tile 0 and of tile 1: O += P V of a buffer,
+//               then the S of two steps later into it.  One issuing thread takes
+//               about as long for a small MMA as the tensor core for one of
+//               N = 128, so each tile has its own
+//   warp 10     TMA: both Q tiles, then K and V blocks of 128 keys into a ring
 //
 // The two tiles share K and V: two heads of one key-value head with the same
 // 128 queries where the group is even, else 256 queries of one head.  Work
 // items are (sequence, tile, heads), the later tiles of a sequence (more
-// keys) first, dealt round to the CTAs.
+// keys) first, dealt to the CTAs forwards and backwards in turn.
 //
 // The running maximum is a reference point only and may lag by 2^8, so almost
-// every block needs one pass over S and no rescaling of O; where a row passes
-// that, its warp rescales O (the previous product has finished by then: S is
-// formed after it) and forms the block again.
+// every step goes without rescaling O; where a row passes that, its warp waits
+// for the product before and rescales O.
 //
 // A key behind a query's last one gets p = 0, but 0 * NaN is not 0: before a
 // block with such keys is used, the softmax warps zero the rows of V behind
@@ -54,11 +56,12 @@ namespace nvq {
 namespace {
 
 constexpr int kTile = 128;           // queries of a tile, keys of a block
-constexpr int kThreads = 320;        // 10 warps: 200 registers a thread
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kStep = 64;            // keys of a step: half a block
+constexpr int kThreads = 352;
+constexpr int kMmaWarp = 8, kLoadWarp = 10;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr float kLazy = 8.0f;
-constexpr int kItemFlags = 8;        // found flags of the last items
+constexpr int kItemFlags = 16;       // found flags of the last items
 
 __device__ unsigned int g_attn_prefill_error_flags = 0;   // bit 0: a wait timed out, bit 1: a bad index
 
@@ -70,7 +73,7 @@ struct Cfg {
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kOffRing = 2 * kBlock;
   static constexpr int kOffBars = kOffRing + kStages * kBlock;
-  static constexpr int kBars = 2 * kStages + 2 + 6 + 1;
+  static constexpr int kBars = 2 * kStages + 2 + 4 + 4 + 2 + 1;
   static constexpr int kOffMisc = kOffBars + 8 * kBars;
   static constexpr int kSmem = kOffMisc + 16 + 4 * kItemFlags + 1024;
 };
@@ -90,10 +93,10 @@ struct Args {
 struct Item {
   int q0, n, k0, m;          // packed rows of the sequence: queries, keys
   int row[2], head[2];       // first query and head of each tile
-  int blocks[2];             // key blocks of each (0: it sees none)
+  int steps[2];              // steps of 64 keys of each (0: it sees none)
   bool on[2];                // whether the tile has queries
   int clean_from;            // the first key that some query does not see
-  __device__ int last() const { return max(blocks[0], blocks[1]); }
+  __device__ int blocks() const { return (max(steps[0], steps[1]) + 1) / 2; }   // K and V blocks loaded
   // keys that query i (of the sequence) sees
   __device__ int limit(int i, int causal) const { return causal ? min(m, i + m - n + 1) : m; }
 };
@@ -113,6 +116,12 @@ __device__ __forceinline__ void sequence(const Args& a, int b, int& q0, int& n, 
   m = k1 - k0;
 }
 
+// Item of this CTA's turn t: every second round is dealt backwards, so that no
+// CTA always gets the longest of a round.
+__device__ __forceinline__ int item_of(int t) {
+  const int G = gridDim.x;
+  return t * G + (t & 1 ? G - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
+}
 // The item's sequence, tile and heads; the whole warp calls.  false: there is
 // no such item.
 __device__ __forceinline__ bool find_item(const Args& a, int x, int lane, Item& it) {
@@ -146,8 +155,8 @@ __device__ __forceinline__ bool find_item(const Args& a, int x, int lane, Item& 
         it.head[s] = a.two_heads ? 2 * pair + s : pair;
         it.on[s] = it.row[s] < it.n;
         const int last_row = min(it.row[s] + kTile, it.n) - 1;
-        it.blocks[s] = it.on[s] ? (max(0, it.limit(last_row, a.causal)) + kTile - 1) / kTile : 0;
-        if (it.blocks[s] > 0) it.clean_from = min(it.clean_from, max(0, it.limit(it.row[s], a.causal)));
+        it.steps[s] = it.on[s] ? (max(0, it.limit(last_row, a.causal)) + kStep - 1) / kStep : 0;
+        if (it.steps[s] > 0) it.clean_from = min(it.clean_from, max(0, it.limit(it.row[s], a.causal)));
       }
       return true;
     }
@@ -195,6 +204,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ void wait_ld_16(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
 // Pairs of fp32 values in one instruction.
 using F2 = unsigned long long;
 __device__ __forceinline__ F2 f2(float x, float y) {
@@ -233,7 +249,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return dev::h2_bits(__floats2half2_rn(lo, hi));
 }
 
-// 128 threads (thread r of them): rows `from`.. of a V block in shared memory:
+// 128 threads (thread r of them): rows `from`.. of a step of V in shared memory:
 // those from `end` on are set to zero, in the others NaN and infinities.
 // *found is set before one is taken out, so whoever finds it gone finds the flag
 // set too.  Eight lanes take a row of 128 bytes; the swizzle only permutes it.
@@ -243,7 +259,7 @@ template <int SUBS, bool BF16>
 __device__ __noinline__ void clean_values(unsigned char* block, int sub_bytes, int from, int end, int r,
                                           volatile int* found) {
   constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
-  for (int row = from + (r >> 3); row < kTile; row += 16) {
+  for (int row = from + (r >> 3); row < kStep; row += 16) {
 #pragma unroll
     for (int i = 0; i < SUBS; ++i) {
       uint4* p = reinterpret_cast<uint4*>(block + i * sub_bytes + row * 128) + (r & 7);
@@ -286,10 +302,10 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   auto kv_full = [&](int s) { return bar(s); };
   auto kv_empty = [&](int s) { return bar(C::kStages + s); };
   const uint32_t q_full = bar(2 * C::kStages), q_empty = bar(2 * C::kStages + 1);
-  auto s_full = [&](int s) { return bar(2 * C::kStages + 2 + s); };
-  auto p_full = [&](int s) { return bar(2 * C::kStages + 4 + s); };
-  auto o_full = [&](int s) { return bar(2 * C::kStages + 6 + s); };
-  const uint32_t mma_done = bar(2 * C::kStages + 8);
+  auto s_full = [&](int s, int b) { return bar(2 * C::kStages + 2 + 2 * s + b); };
+  auto p_full = [&](int s, int b) { return bar(2 * C::kStages + 6 + 2 * s + b); };
+  auto o_done = [&](int s) { return bar(2 * C::kStages + 10 + s); };
+  const uint32_t mma_done = bar(2 * C::kStages + 12);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* found = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);
@@ -298,16 +314,18 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(kv_full(s), 1);
-      ptx::mbar_init(kv_empty(s), 1);
+      ptx::mbar_init(kv_empty(s), 2);      // both tiles
     }
     ptx::mbar_init(q_full, 1);
-    ptx::mbar_init(q_empty, 1);
+    ptx::mbar_init(q_empty, 2);
     for (int s = 0; s < 2; ++s) {
-      ptx::mbar_init(s_full(s), 1);
-      ptx::mbar_init(p_full(s), 4);
-      ptx::mbar_init(o_full(s), 1);
+      for (int b = 0; b < 2; ++b) {
+        ptx::mbar_init(s_full(s, b), 1);
+        ptx::mbar_init(p_full(s, b), 4);
+      }
+      ptx::mbar_init(o_done(s), 1);
     }
-    ptx::mbar_init(mma_done, 1);
+    ptx::mbar_init(mma_done, 2);
     *abort_flag = 0;
     for (int i = 0; i < kItemFlags; ++i) found[i] = 0;
     ptx::fence_mbar_init();
@@ -338,8 +356,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
     fail();
     return false;
   };
-  // tensor memory: S (and P) of tile s at 128 s, O at 256 + 128 s
-  const int G = gridDim.x;
+  // tensor memory: S (and P) of tile s, buffer b at 128 s + 64 b, O at 256 + 128 s
 
   if (warp == kLoadWarp) {
     // --------------------------------- copies ---------------------------------
@@ -359,22 +376,22 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       return true;
     };
     int items = 0;
-    for (int x = blockIdx.x; ok && x < a.max_items && find_item(a, x, lane, it); x += G) {
-      if (it.last() == 0) continue;
+    for (int t = 0, x; ok && (x = item_of(t), t * static_cast<int>(gridDim.x) < a.max_items); ++t) {
+      if (!find_item(a, x, lane, it) || it.blocks() == 0) continue;
       ok = warp_wait(q_empty, (items & 1) ^ 1);
       if (!ok) break;
       if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(q_full, (it.blocks[0] > 0 ? C::kBlock : 0) + (it.blocks[1] > 0 ? C::kBlock : 0));
+        ptx::mbar_arrive_expect_tx(q_full, (it.steps[0] > 0 ? C::kBlock : 0) + (it.steps[1] > 0 ? C::kBlock : 0));
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-          if (it.blocks[s] > 0)
+          if (it.steps[s] > 0)
             for (int i = 0; i < C::kSubs; ++i)
               ptx::tma_load_2d(base + s * C::kBlock + i * C::kSub, &q_map, it.head[s] * D + 64 * i, it.q0 + it.row[s], q_full);
       }
       __syncwarp();
       ++items;
       const int col = it.head[0] / a.group * D;
-      for (int j = 0; ok && j < it.last(); ++j)
+      for (int j = 0; ok && j < it.blocks(); ++j)
         ok = block(&k_map, col, it.k0 + j * kTile) && block(&v_map, col, it.k0 + j * kTile);
     }
     if (*abort_flag) {
@@ -383,75 +400,73 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       for (int i = max(0, g - C::kStages); i < g; ++i)
         ptx::mbar_wait_bounded(kv_full(i % C::kStages), (i / C::kStages) & 1, nullptr, kWaitLimitNs);
     }
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------- MMAs ----------------------------------
+  } else if (warp >= kMmaWarp) {
+    // ------------------------------ MMAs of tile s ------------------------------
     constexpr uint32_t kFmt = BF16 ? (1u << 7) | (1u << 10) : 0u;
-    constexpr uint32_t idesc_s = ptx::idesc_f16_f32(kTile, kTile) | kFmt;
+    constexpr uint32_t idesc_s = ptx::idesc_f16_f32(kTile, kStep) | kFmt;
     constexpr uint32_t idesc_o = ptx::idesc_f16_f32(kTile, D) | kFmt | (1u << 16);   // V: columns contiguous
+    const int s = warp - kMmaWarp;
+    const uint32_t t_s = tmem + 128 * s, t_o = tmem + 256 + 128 * s;
+    const uint64_t q = ptx::sw128_kmajor_desc(base + s * C::kBlock);
     int g = 0, items = 0;
-    int p_count[2] = {0, 0};
+    uint32_t p_par = 0;          // parity of each buffer's next P
     bool ok = true;
     Item it;
     auto ring = [&](int i) { return base + C::kOffRing + (i % C::kStages) * C::kBlock; };
     auto wait_block = [&](int i) { return warp_wait(kv_full(i % C::kStages), (i / C::kStages) & 1); };
-    auto scores = [&](int s, int kblock) {       // lane 0
-      const uint64_t q = ptx::sw128_kmajor_desc(base + s * C::kBlock), k = ptx::sw128_kmajor_desc(ring(kblock));
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint32_t off = ((i / 4) * C::kSub + (i % 4) * 32) >> 4;
-        mma_f16_ss(tmem + 128 * s, q + off, k + off, idesc_s, i > 0);
-      }
-      ptx::mma_commit(s_full(s));
-    };
-    auto values = [&](int s, int vblock, bool first) {
-      const uint64_t v = sw128_mnmajor_desc(ring(vblock), C::kSub);
-#pragma unroll
-      for (int i = 0; i < kTile / 16; ++i)
-        ptx::mma_f16_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * i, v + ((i * 16 * 128) >> 4), idesc_o, !first || i > 0);
-    };
-    for (int x = blockIdx.x; ok && x < a.max_items && find_item(a, x, lane, it); x += G) {
-      const int N = it.last();
-      if (N == 0) continue;
-      ok = warp_wait(q_full, items & 1) && wait_block(g);
+    for (int t = 0, x; ok && (x = item_of(t), t * static_cast<int>(gridDim.x) < a.max_items); ++t) {
+      if (!find_item(a, x, lane, it) || it.blocks() == 0) continue;
+      const int N = it.blocks(), steps = s ? it.steps[1] : it.steps[0];
+      ok = warp_wait(q_full, items & 1);
       if (!ok) break;
-      if (lane == 0) {
-        // the flag of an item to come: of those before this one only the last
-        // can still be read
-        found[(items + 2) % kItemFlags] = 0;
-        ptx::tc_fence_after();
+      // the flag of an item to come; the ring keeps the tiles fewer items apart
+      if (s == 0 && lane == 0) found[(items + kItemFlags / 2) % kItemFlags] = 0;
+      auto scores = [&](int i) {       // S of step i
+        const int k = g + (i & ~1);
+        if (!(i & 1) && !wait_block(k)) return false;
+        if (lane == 0) {
+          ptx::tc_fence_after();
+          const uint64_t kd = ptx::sw128_kmajor_desc(ring(k) + (i & 1) * kStep * 128);
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-          if (it.blocks[s] > 0) scores(s, g);
-        ptx::mma_commit(kv_empty(g % C::kStages));
-        if (N == 1) ptx::mma_commit(q_empty);
-      }
-      __syncwarp();
-      ++items;
-      for (int j = 0; ok && j < N; ++j) {
-        const int v = g + 2 * j + 1, k = v + 1;       // ring places of V_j and K_j+1
-        ok = wait_block(v) && (j + 1 == N || wait_block(k));
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (!ok || j >= it.blocks[s]) continue;
-          ok = warp_wait(p_full(s), p_count[s]++ & 1);
-          if (ok && lane == 0) {
-            ptx::tc_fence_after();
-            values(s, v, j == 0);
-            if (j + 1 < it.blocks[s])
-              scores(s, k);
-            else
-              ptx::mma_commit(o_full(s));
+          for (int e = 0; e < D / 16; ++e) {
+            const uint32_t off = ((e / 4) * C::kSub + (e % 4) * 32) >> 4;
+            mma_f16_ss(t_s + kStep * (i & 1), q + off, kd + off, idesc_s, e > 0);
           }
-          __syncwarp();
-        }
-        if (ok && lane == 0) {
-          ptx::mma_commit(kv_empty(v % C::kStages));
-          if (j + 1 < N) ptx::mma_commit(kv_empty(k % C::kStages));
-          if (j + 2 == N) ptx::mma_commit(q_empty);
+          ptx::mma_commit(s_full(s, i & 1));
+          if ((i & 1) || i + 1 == steps) ptx::mma_commit(kv_empty(k % C::kStages));
+          if (i + 1 == steps) ptx::mma_commit(q_empty);
         }
         __syncwarp();
+        return true;
+      };
+      if (steps > 0) ok = scores(0);
+      if (ok && steps > 1) ok = scores(1);
+      for (int i = 0; ok && i < steps; ++i) {
+        const int v = g + (i | 1), b = i & 1;
+        ok = (b || wait_block(v)) && warp_wait(p_full(s, b), (p_par >> b) & 1);
+        if (!ok) break;
+        p_par ^= 1u << b;
+        if (lane == 0) {
+          ptx::tc_fence_after();
+          const uint64_t vd = sw128_mnmajor_desc(ring(v) + b * kStep * 128, C::kSub);
+#pragma unroll
+          for (int e = 0; e < kStep / 16; ++e)
+            ptx::mma_f16_ts(t_o, t_s + kStep * b + 8 * e, vd + ((e * 16 * 128) >> 4), idesc_o, i > 0 || e > 0);
+          ptx::mma_commit(o_done(s));
+          if (b || i + 1 == steps) ptx::mma_commit(kv_empty(v % C::kStages));
+        }
+        __syncwarp();
+        if (i + 2 < steps) ok = scores(i + 2);
       }
+      // blocks that only the other tile uses
+      for (int i = g + 2 * ((steps + 1) / 2); ok && i < g + 2 * N; ++i) {
+        ok = wait_block(i);
+        if (ok && lane == 0) ptx::mbar_arrive(kv_empty(i % C::kStages));
+        __syncwarp();
+      }
+      if (ok && steps == 0 && lane == 0) ptx::mbar_arrive(q_empty);
       g += 2 * N;
+      ++items;
     }
     // no MMA may still use shared or tensor memory when they are released
     if (lane == 0) ptx::mma_commit(mma_done);
@@ -464,132 +479,114 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + 128 * s, t_o = tmem + lanes + 256 + 128 * s;
     const float c = a.scale_log2;
-    int g = 0, count = 0, o_count = 0, items = 0;
+    int g = 0, items = 0;
+    uint32_t s_par = 0;                            // parity of each buffer's next S
+    int sent = 0;                                  // steps handed on, over all items
     bool ok = true;
     Item it;
-    for (int x = blockIdx.x; ok && x < a.max_items && find_item(a, x, lane, it); x += G) {
-      const bool counted = it.last() > 0;
+    for (int t = 0, x; ok && (x = item_of(t), t * static_cast<int>(gridDim.x) < a.max_items); ++t) {
+      if (!find_item(a, x, lane, it)) continue;
       const int item = items;
       const int g0 = g;                            // ring place of K_0
-      if (counted) ++items;
-      g += 2 * it.last();
+      if (it.blocks() > 0) ++items;
+      g += 2 * it.blocks();
       // this tile's values (selected, so that they stay in registers)
       if (!(s ? it.on[1] : it.on[0])) continue;
       const int row = (s ? it.row[1] : it.row[0]) + r;       // query of the sequence
-      const int blocks = s ? it.blocks[1] : it.blocks[0], head = s ? it.head[1] : it.head[0];
+      const int steps = s ? it.steps[1] : it.steps[0], head = s ? it.head[1] : it.head[0];
       const int limit = it.limit(row, a.causal);
       float ref = 0.0f, l = 0.0f;                  // reference (a score); sum
-      for (int j = 0; ok && j < blocks; ++j) {
-        ok = warp_wait(s_full(s), count++ & 1);
+      for (int i = 0; ok && i < steps; ++i) {
+        const int b = i & 1;
+        ok = warp_wait(s_full(s, b), (s_par >> b) & 1);
         if (!ok) break;
+        s_par ^= 1u << b;
         ptx::tc_fence_after();
-        const int seen = limit - j * kTile;        // keys of the block that the row sees
-        const bool masked = __any_sync(0xffffffffu, seen < kTile);
-        uint32_t p[64];
-        // One pass: the exponentials against the reference, their sum, and
-        // the block's maximum (NaN if a score is).  Returns the sum.
-        float top;
-        auto hide = [&](uint32_t (&w)[32], int col) {
-          if (masked) {
+        const int seen = limit - i * kStep;        // keys of the step that the row sees
+        uint32_t v[2][32];
+        ptx::tmem_ld_32cols(t_s + kStep * b, v[0]);
+        ptx::tmem_ld_32cols(t_s + kStep * b + 32, v[1]);
+        wait_ld_32(v[0]);
+        wait_ld_32(v[1]);
+        if (__any_sync(0xffffffffu, seen < kStep)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (col + i >= seen) w[i] = 0xFF800000u;       // -infinity
-          }
-        };
-        auto pass = [&]() -> float {
-          F2 sum0 = f2(0.0f), sum1 = f2(0.0f);
-          const F2 n2 = f2(-ref), c2 = f2(c);
-          float top1 = -INFINITY;
-          top = -INFINITY;
-          uint32_t v[2][32];
-          ptx::tmem_ld_32cols(t_s, v[0]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t(&w)[32] = v[q & 1];
-            wait_ld_32(w);
-            if (q < 3) ptx::tmem_ld_32cols(t_s + 32 * (q + 1), v[(q + 1) & 1]);
-            hide(w, 32 * q);
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              top = max3_nan(top, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
-              top1 = max3_nan(top1, __uint_as_float(w[i + 2]), __uint_as_float(w[i + 3]));
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              // the difference comes first: it is exact where scores are
-              // near their maximum, however large they are
-              const float2 t = split2(mul2(add2(f2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), n2), c2));
-              const float2 e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
-              (i & 2 ? sum1 : sum0) = add2(i & 2 ? sum1 : sum0, f2(e.x, e.y));
-              p[16 * q + i / 2] = pack2<BF16>(e.x, e.y);
-            }
-          }
-          top = max3_nan(top, top1, top1);
-          const float2 total = split2(add2(sum0, sum1));
-          // a score that is NaN or +infinity makes the row NaN
-          return top < INFINITY ? total.x + total.y : __int_as_float(0x7FFFFFFF);
-        };
-        if (j == 0) {
-          // the first reference: the largest of the first 32 scores
-          uint32_t w[32];
-          ptx::tmem_ld_32cols(t_s, w);
-          wait_ld_32(w);
-          hide(w, 0);
-          float first = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) first = max3_nan(first, __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
-          if (fabsf(first) < INFINITY) ref = first;
+          for (int e = 0; e < kStep; ++e)
+            if (e >= seen) v[e / 32][e % 32] = 0xFF800000u;       // -infinity
         }
-        float sum = pass();
-        const bool grow = (top - ref) * c > kLazy;
-        if (__any_sync(0xffffffffu, grow)) {
-          // a new reference for the rows that passed theirs
-          const float f = grow ? exp2_approx((ref - top) * c) : 1.0f;
-          if (grow) ref = top;
-          l *= f;
-          if (j > 0) {
-            // O of the blocks so far: their product finished before this S
+        // the step's maximum (NaN if a score is)
+        float top = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t v[32];
-              ptx::tmem_ld_32cols(t_o + 32 * q, v);
-              wait_ld_32(v);
+        for (int e = 0; e < 32; e += 2) {
+          top = max3_nan(top, __uint_as_float(v[0][e]), __uint_as_float(v[0][e + 1]));
+          top1 = max3_nan(top1, __uint_as_float(v[1][e]), __uint_as_float(v[1][e + 1]));
+        }
+        top = max3_nan(top, top1, top1);
+        if (i == 0) {
+          if (fabsf(top) < INFINITY) ref = top;
+        } else {
+          const bool grow = (top - ref) * c > kLazy;
+          if (__any_sync(0xffffffffu, grow)) {
+            // a new reference for the rows that passed theirs.  O holds the
+            // steps before, once the last of their products is done (the one
+            // before that is: this S was formed after it)
+            const float f = grow ? exp2_approx((ref - top) * c) : 1.0f;
+            if (grow) ref = top;
+            l *= f;
+            ok = warp_wait(o_done(s), (sent - 1) & 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-              ptx::tmem_st_32cols(t_o + 32 * q, v);
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t w[16];
+              ptx::tmem_ld_16cols(t_o + 16 * q, w);
+              wait_ld_16(w);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+              ptx::tmem_st_16cols(t_o + 16 * q, w);
             }
           }
-          sum = pass();
         }
-        l += sum;
+        // the exponentials.  The difference comes first: it is exact where
+        // scores are near their maximum, however large they are
+        F2 sum0 = f2(0.0f), sum1 = f2(0.0f);
+        const F2 n2 = f2(-ref), c2 = f2(c);
+        uint32_t p[32];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t v[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = p[32 * q + i];
-          ptx::tmem_st_32cols(t_s + 32 * q, v);
+        for (int e = 0; e < kStep; e += 2) {
+          const float2 u = split2(mul2(add2(f2(__uint_as_float(v[e / 32][e % 32]), __uint_as_float(v[e / 32][e % 32 + 1])), n2), c2));
+          const float2 y = make_float2(exp2_approx(u.x), exp2_approx(u.y));
+          (e & 2 ? sum1 : sum0) = add2(e & 2 ? sum1 : sum0, f2(y.x, y.y));
+          p[e / 2] = pack2<BF16>(y.x, y.y);
         }
-        if ((j + 1) * kTile > it.clean_from) {
-          // V_j has keys that some query does not see (its place in the ring is
-          // this one until P is released)
-          const int v = g0 + 2 * j + 1;
-          ok = warp_wait(kv_full(v % C::kStages), (v / C::kStages) & 1);
+        const float2 sum = split2(add2(sum0, sum1));
+        // a score that is NaN or +infinity makes the row NaN
+        l += top < INFINITY ? sum.x + sum.y : __int_as_float(0x7FFFFFFF);
+        ptx::tmem_st_32cols(t_s + kStep * b, p);
+        if ((i + 1) * kStep > it.clean_from) {
+          // V has keys here that some query does not see (its place in the ring
+          // is this one until P is released)
+          const int vb = g0 + (i | 1);
+          ok = warp_wait(kv_full(vb % C::kStages), (vb / C::kStages) & 1);
           if (!ok) break;
-          clean_values<C::kSubs, BF16>(smem + C::kOffRing + (v % C::kStages) * C::kBlock, C::kSub,
-                                       max(0, it.clean_from - j * kTile), it.m - j * kTile, r,
+          clean_values<C::kSubs, BF16>(smem + C::kOffRing + (vb % C::kStages) * C::kBlock + b * kStep * 128, C::kSub,
+                                       max(0, it.clean_from - i * kStep), it.m - i * kStep, r,
                                        found + item % kItemFlags);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(p_full(s));
+        if (lane == 0) ptx::mbar_arrive(p_full(s, b));
+        ++sent;
       }
       if (!ok) break;
       // -------- the tile's results
-      const bool some = blocks > 0;
+      const bool some = steps > 0;
       if (some) {
-        ok = warp_wait(o_full(s), o_count++ & 1);
+        // the last two products, one after the other: a parity tells only two
+        // phases apart
+        if (steps > 1) ok = warp_wait(o_done(s), (sent - 2) & 1);
+        ok = ok && warp_wait(o_done(s), (sent - 1) & 1);
         if (!ok) break;
         ptx::tc_fence_after();
       }
