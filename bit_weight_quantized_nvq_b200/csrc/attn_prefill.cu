@@ -28,9 +28,11 @@
 // items are (sequence, tile, heads), the later tiles of a sequence (more
 // keys) first, dealt to the CTAs forwards and backwards in turn.
 //
-// The running maximum is a reference point only and may lag by 2^8, so almost
-// every step goes without rescaling O; where a row passes that, its warp waits
-// for the product before and rescales O.
+// The running maximum is a reference point only: the first step's maximum,
+// kept while no later step's exponentials add up to more than 2^8 (then none of
+// them is above that).  So a step costs no search for its maximum and no
+// rescaling of O; where a row passes the mark, its warp searches, waits for the
+// product before, rescales O and forms the step again.
 //
 // A key behind a query's last one gets p = 0, but 0 * NaN is not 0: before a
 // block with such keys is used, the softmax warps zero the rows of V behind
@@ -60,7 +62,8 @@ constexpr int kStep = 64;            // keys of a step: half a block
 constexpr int kThreads = 352;
 constexpr int kMmaWarp = 8, kLoadWarp = 10;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
-constexpr float kLazy = 8.0f;
+constexpr float kLazy = 256.0f;       // how far a step's exponentials may add up before the reference moves
+constexpr float kLarge = 1024.0f;     // exponents from here on are formed as differences first
 constexpr int kItemFlags = 16;       // found flags of the last items
 
 __device__ unsigned int g_attn_prefill_error_flags = 0;   // bit 0: a wait timed out, bit 1: a bad index
@@ -232,6 +235,11 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
   F2 r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 // The largest of three; NaN if one is.
@@ -513,25 +521,58 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           for (int e = 0; e < kStep; ++e)
             if (e >= seen) v[e / 32][e % 32] = 0xFF800000u;       // -infinity
         }
-        // the step's maximum (NaN if a score is)
-        float top = -INFINITY, top1 = -INFINITY;
+        // the step's maximum (NaN if a score is); it is not needed as a rule
+        auto largest = [&]() -> float {
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          top = max3_nan(top, __uint_as_float(v[0][e]), __uint_as_float(v[0][e + 1]));
-          top1 = max3_nan(top1, __uint_as_float(v[1][e]), __uint_as_float(v[1][e + 1]));
-        }
-        top = max3_nan(top, top1, top1);
+          for (int e = 0; e < kStep; e += 2)
+            top[e / 2 % 4] = max3_nan(top[e / 2 % 4], __uint_as_float(v[e / 32][e % 32]), __uint_as_float(v[e / 32][e % 32 + 1]));
+          return max3_nan(max3_nan(top[0], top[1], top[2]), top[3], top[3]);
+        };
         if (i == 0) {
+          const float top = largest();
           if (fabsf(top) < INFINITY) ref = top;
-        } else {
-          const bool grow = (top - ref) * c > kLazy;
-          if (__any_sync(0xffffffffu, grow)) {
-            // a new reference for the rows that passed theirs.  O holds the
-            // steps before, once the last of their products is done (the one
-            // before that is: this S was formed after it)
-            const float f = grow ? exp2_approx((ref - top) * c) : 1.0f;
-            if (grow) ref = top;
-            l *= f;
+        }
+        // The exponentials against the reference, and their sum.  Where scores
+        // are large the difference comes first: it is exact near the maximum.
+        auto form = [&](auto large) -> float {
+          F2 sum0 = f2(0.0f), sum1 = f2(0.0f);
+          const F2 n2 = decltype(large)::value ? f2(-ref) : f2(-ref * c), c2 = f2(c);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const F2 x = f2(__uint_as_float(v[h][e]), __uint_as_float(v[h][e + 1]));
+              const float2 u = split2(decltype(large)::value ? mul2(add2(x, n2), c2) : fma2(x, c2, n2));
+              const float2 y = make_float2(exp2_approx(u.x), exp2_approx(u.y));
+              (e & 2 ? sum1 : sum0) = add2(e & 2 ? sum1 : sum0, f2(y.x, y.y));
+              p[e / 2] = pack2<BF16>(y.x, y.y);
+            }
+            ptx::tmem_st_16cols(t_s + kStep * b + 16 * h, p);
+          }
+          const float2 sum = split2(add2(sum0, sum1));
+          return sum.x + sum.y;
+        };
+        using Yes = std::integral_constant<bool, true>;
+        using No = std::integral_constant<bool, false>;
+        // No exponential is above their sum: while that stays below 2^8 the
+        // reference may lag.  Else (NaN among them) the step's maximum becomes
+        // the reference, and the step is formed again.
+        bool large = false;
+        float sum;
+        for (int round = 0;; ++round) {
+          large |= __any_sync(0xffffffffu, fabsf(ref * c) > kLarge);
+          sum = large ? form(Yes{}) : form(No{});
+          const bool grow = !(sum <= kLazy);
+          if (round > 0 || !__any_sync(0xffffffffu, grow)) break;
+          const float top = largest();
+          const float f = grow ? exp2_approx((ref - top) * c) : 1.0f;
+          if (grow) ref = top;
+          l *= f;
+          if (i > 0) {
+            // O holds the steps before, once the last of their products is
+            // done (the one before that is: this S was formed after it)
             ok = warp_wait(o_done(s), (sent - 1) & 1);
             if (!ok) break;
             ptx::tc_fence_after();
@@ -546,22 +587,8 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
             }
           }
         }
-        // the exponentials.  The difference comes first: it is exact where
-        // scores are near their maximum, however large they are
-        F2 sum0 = f2(0.0f), sum1 = f2(0.0f);
-        const F2 n2 = f2(-ref), c2 = f2(c);
-        uint32_t p[32];
-#pragma unroll
-        for (int e = 0; e < kStep; e += 2) {
-          const float2 u = split2(mul2(add2(f2(__uint_as_float(v[e / 32][e % 32]), __uint_as_float(v[e / 32][e % 32 + 1])), n2), c2));
-          const float2 y = make_float2(exp2_approx(u.x), exp2_approx(u.y));
-          (e & 2 ? sum1 : sum0) = add2(e & 2 ? sum1 : sum0, f2(y.x, y.y));
-          p[e / 2] = pack2<BF16>(y.x, y.y);
-        }
-        const float2 sum = split2(add2(sum0, sum1));
-        // a score that is NaN or +infinity makes the row NaN
-        l += top < INFINITY ? sum.x + sum.y : __int_as_float(0x7FFFFFFF);
-        ptx::tmem_st_32cols(t_s + kStep * b, p);
+        if (!ok) break;
+        l += sum;
         if ((i + 1) * kStep > it.clean_from) {
           // V has keys here that some query does not see (its place in the ring
           // is this one until P is released)
