@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from contextlib import nullcontext
 
 import numpy as np
 import torch
@@ -350,47 +351,62 @@ def _dtype(t: torch.Tensor) -> int:
     return code
 
 
-def _rows(name: str, t: torch.Tensor, heads: int, dim: int, like: torch.Tensor | None = None) -> int:
+def _rows(name: str, t: torch.Tensor, heads: int, dim: int, like: torch.Tensor) -> int:
     """Elements between the rows of t [rows, heads, dim], whose rows must be
     contiguous; on the device and of the type of `like`."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name}: [rows, {heads}, {dim}] expected, not {tuple(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    if like is not None and (t.device != like.device or t.dtype != like.dtype):
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name}: [rows, {heads}, {dim}] expected, not {tuple(shape)}")
+    if t.device != like.device or t.dtype != like.dtype:
         raise ValueError(f"{name}: {like.dtype} on {like.device} expected")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    width = heads * dim
+    if t.is_contiguous():
+        return width
+    strides = t.stride()
+    if strides[2] != 1 or (heads > 1 and strides[1] != dim):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return strides[0] if shape[0] > 1 else width
 
 
-def _index(name: str, t: torch.Tensor, like: torch.Tensor, *shape: int) -> None:
-    if t.dtype != torch.int32 or t.device != like.device or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous int32 on {like.device} expected")
-    if tuple(t.shape) != shape:
+def _index(name: str, t: torch.Tensor, dev: torch.device, *shape: int) -> int:
+    if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous int32 on {dev} expected")
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {shape} expected, not {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _cache(cache, like: torch.Tensor) -> KVCache:
+def _cache(cache, dev: torch.device) -> KVCache:
     """The C descriptor of (k_codes, k_scales, v_codes, v_scales)."""
     kc, ks, vc, vs = cache
-    if kc.dim() != 4 or ks.shape != kc.shape[:3] + (kc.shape[3] // 32,):
-        raise ValueError("cache: codes [pages, kv_heads, page_size, head_dim] and scales "
-                         "[pages, kv_heads, page_size, head_dim / 32] expected")
-    if vc.shape != kc.shape or vs.shape != ks.shape:
-        raise ValueError("cache: keys and values differ in shape")
-    for t, dt in ((kc, torch.int8), (ks, torch.float16), (vc, torch.int8), (vs, torch.float16)):
-        if t.dtype != dt or t.device != like.device or not t.is_contiguous():
-            raise ValueError(f"cache: contiguous int8 codes and float16 scales on {like.device} expected")
-    return KVCache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), *kc.shape)
+    shape = kc.shape
+    if len(shape) != 4 or vc.shape != shape or ks.shape != vs.shape \
+            or ks.shape != (shape[0], shape[1], shape[2], shape[3] // 32):
+        raise ValueError("cache: keys and values as codes [pages, kv_heads, page_size, head_dim] "
+                         "and scales [pages, kv_heads, page_size, head_dim / 32] expected")
+    for codes, scales in ((kc, ks), (vc, vs)):
+        if codes.dtype != torch.int8 or scales.dtype != torch.float16 or codes.device != dev \
+                or scales.device != dev or not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError(f"cache: contiguous int8 codes and float16 scales on {dev} expected")
+    return KVCache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), *shape)
 
 
-def _batch(cache, like, cu_seqlens, seq_lens, block_table):
-    B = seq_lens.shape[0]
-    max_pages = block_table.shape[-1]
-    _index("seq_lens", seq_lens, like, B)
-    _index("block_table", block_table, like, B, max_pages)
-    if cu_seqlens is not None:
-        _index("cu_seqlens", cu_seqlens, like, B + 1)
-    return B, max_pages
+def _launch(dev: torch.device, stream, name: str, *args) -> None:
+    """Call an entry point with `dev` current, on its current stream unless
+    another is given."""
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: tensors on a CUDA device expected, not {dev}")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _check(name, getattr(_lib, name)(*args, _stream(stream)))
+        return
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        stream = _stream(stream)
+    status = getattr(_lib, name)(*args, stream)
+    if status != NVQ_OK:
+        raise NVQError(name, status)
 
 
 def kv_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device="cuda"):
@@ -410,17 +426,16 @@ def kv_write(cache, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
     or bfloat16; packed by sequence, the last positions of each) into the
     cache's pages (nvq_kv_write).  cu_seqlens int32 [B + 1], seq_lens int32
     [B] (these rows included), block_table int32 [B, max_pages]."""
-    dt = _dtype(k)
-    c = _cache(cache, k)
-    ks = _rows("k", k, c.n_kv_heads, c.head_dim)
-    vs = _rows("v", v, c.n_kv_heads, c.head_dim, k)
-    if v.shape[0] != k.shape[0]:
+    dt, dev = _dtype(k), k.device
+    c = _cache(cache, dev)
+    heads, dim, rows = c.n_kv_heads, c.head_dim, k.shape[0]
+    ks, vs = _rows("k", k, heads, dim, k), _rows("v", v, heads, dim, k)
+    if v.shape[0] != rows:
         raise ValueError("v: as many rows as k expected")
-    B, max_pages = _batch(cache, k, cu_seqlens, seq_lens, block_table)
-    with torch.cuda.device(k.device):
-        _check("nvq_kv_write", _lib.nvq_kv_write(
-            ctypes.byref(c), _ptr(k), ks, _ptr(v), vs, dt, _ptr(cu_seqlens), _ptr(seq_lens),
-            _ptr(block_table), B, max_pages, k.shape[0], _stream(stream)))
+    B, cols = seq_lens.shape[0], block_table.shape[-1]
+    _launch(dev, stream, "nvq_kv_write", c, k.data_ptr(), ks, v.data_ptr(), vs, dt,
+            _index("cu_seqlens", cu_seqlens, dev, B + 1), _index("seq_lens", seq_lens, dev, B),
+            _index("block_table", block_table, dev, B, cols), B, cols, rows)
 
 
 def kv_read(cache, cu_seqlens: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
@@ -430,23 +445,21 @@ def kv_read(cache, cu_seqlens: torch.Tensor, seq_lens: torch.Tensor, block_table
     cu_seqlens[b] positions of each sequence, packed; returns (k, v) of
     [rows, n_kv_heads, head_dim].  rows >= cu_seqlens[B]; rows behind the
     last sequence are left as they were."""
-    c = _cache(cache, cache[0])
     dev = cache[0].device
-    shape = (rows, c.n_kv_heads, c.head_dim)
+    c = _cache(cache, dev)
+    heads, dim = c.n_kv_heads, c.head_dim
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=dev)
+        k = torch.empty((rows, heads, dim), dtype=dtype, device=dev)
     if v is None:
-        v = torch.empty(shape, dtype=k.dtype, device=dev)
+        v = torch.empty((rows, heads, dim), dtype=k.dtype, device=dev)
     dt = _dtype(k)
-    ks = _rows("k", k, c.n_kv_heads, c.head_dim)
-    vs = _rows("v", v, c.n_kv_heads, c.head_dim, k)
+    ks, vs = _rows("k", k, heads, dim, k), _rows("v", v, heads, dim, k)
     if k.shape[0] != rows or v.shape[0] != rows or k.device != dev:
         raise ValueError(f"k, v: {rows} rows on {dev} expected")
-    B, max_pages = _batch(cache, k, cu_seqlens, seq_lens, block_table)
-    with torch.cuda.device(dev):
-        _check("nvq_kv_read", _lib.nvq_kv_read(
-            ctypes.byref(c), _ptr(k), ks, _ptr(v), vs, dt, _ptr(cu_seqlens), _ptr(seq_lens),
-            _ptr(block_table), B, max_pages, rows, _stream(stream)))
+    B, cols = seq_lens.shape[0], block_table.shape[-1]
+    _launch(dev, stream, "nvq_kv_read", c, k.data_ptr(), ks, v.data_ptr(), vs, dt,
+            _index("cu_seqlens", cu_seqlens, dev, B + 1), _index("seq_lens", seq_lens, dev, B),
+            _index("block_table", block_table, dev, B, cols), B, cols, rows)
     return k, v
 
 
@@ -459,29 +472,33 @@ def attn_decode(cache, q: torch.Tensor, seq_lens: torch.Tensor, block_table: tor
     returns out of q's shape and type.  counters: device int32
     [B * n_heads], zero before the first call, left zero; calls that may
     overlap need their own.  scale: 1/sqrt(head_dim) unless given."""
-    dt = _dtype(q)
-    c = _cache(cache, q)
-    B, max_pages = _batch(cache, q, None, seq_lens, block_table)
+    dt, dev = _dtype(q), q.device
+    c = _cache(cache, dev)
+    B, cols = seq_lens.shape[0], block_table.shape[-1]
     H, D = q.shape[1], c.head_dim
-    qs = _rows("q", q, H, D)
+    qs = _rows("q", q, H, D, q)
     if q.shape[0] != B:
         raise ValueError(f"q: {B} rows expected, one per sequence")
-    if counters.dtype != torch.int32 or counters.device != q.device or not counters.is_contiguous() \
+    if counters.dtype != torch.int32 or counters.device != dev or not counters.is_contiguous() \
             or counters.numel() < B * H:
-        raise ValueError(f"counters: contiguous int32 [{B * H}] on {q.device} expected")
+        raise ValueError(f"counters: contiguous int32 [{B * H}] on {dev} expected")
     if out is None:
-        out = torch.empty((B, H, D), dtype=q.dtype, device=q.device)
-    os_ = _rows("out", out, H, D, q)
-    if out.shape[0] != B:
-        raise ValueError(f"out: {B} rows expected")
-    with torch.cuda.device(q.device):
-        if workspace is None:
-            nbytes = int(_lib.nvq_attn_decode_workspace_size(B, H, c.n_kv_heads, D))
-            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
-        _check("nvq_attn_decode", _lib.nvq_attn_decode(
-            ctypes.byref(c), _ptr(q), qs, dt, _ptr(seq_lens), _ptr(block_table), B, max_pages,
-            H, float(D ** -0.5 if scale is None else scale), _ptr(out), os_, _ptr(counters),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        out = torch.empty((B, H, D), dtype=q.dtype, device=dev)
+        os_ = H * D
+    else:
+        os_ = _rows("out", out, H, D, q)
+        if out.shape[0] != B:
+            raise ValueError(f"out: {B} rows expected")
+    if workspace is None:
+        if dev.type != "cuda":
+            raise ValueError(f"nvq_attn_decode: tensors on a CUDA device expected, not {dev}")
+        with torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else nullcontext():
+            nbytes = _lib.nvq_attn_decode_workspace_size(B, H, c.n_kv_heads, D)
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    _launch(dev, stream, "nvq_attn_decode", c, q.data_ptr(), qs, dt,
+            _index("seq_lens", seq_lens, dev, B), _index("block_table", block_table, dev, B, cols),
+            B, cols, H, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+            counters.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
 
 
@@ -493,31 +510,27 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.
     head_dim], k and v [total_k, n_kv_heads, head_dim], float16 or bfloat16;
     cu_q, cu_k int32 [B + 1] (cu_k: cu_q unless given); returns out of q's
     shape and type, rows from cu_q[B] on left as they were."""
-    dt = _dtype(q)
+    dt, dev = _dtype(q), q.device
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k: [rows, heads, head_dim] expected")
-    H, D = q.shape[1], q.shape[2]
-    Hk = k.shape[1]
+    rows, H, D = q.shape
+    keys, Hk = k.shape[0], k.shape[1]
     if cu_k is None:
         cu_k = cu_q
-    qs = _rows("q", q, H, D)
-    ks = _rows("k", k, Hk, D, q)
-    vs = _rows("v", v, Hk, D, q)
-    if v.shape[0] != k.shape[0]:
+    qs, ks, vs = _rows("q", q, H, D, q), _rows("k", k, Hk, D, q), _rows("v", v, Hk, D, q)
+    if v.shape[0] != keys:
         raise ValueError("v: as many rows as k expected")
     B = cu_q.shape[0] - 1
-    _index("cu_q", cu_q, q, B + 1)
-    _index("cu_k", cu_k, q, B + 1)
     if out is None:
-        out = torch.empty((q.shape[0], H, D), dtype=q.dtype, device=q.device)
-    os_ = _rows("out", out, H, D, q)
-    if out.shape[0] != q.shape[0]:
-        raise ValueError(f"out: {q.shape[0]} rows expected")
-    with torch.cuda.device(q.device):
-        _check("nvq_attn_prefill", _lib.nvq_attn_prefill(
-            _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, dt, _ptr(cu_q), _ptr(cu_k), B, q.shape[0],
-            k.shape[0], H, Hk, D, float(D ** -0.5 if scale is None else scale), 1 if causal else 0,
-            _ptr(out), os_, _stream(stream)))
+        out = torch.empty((rows, H, D), dtype=q.dtype, device=dev)
+        os_ = H * D
+    else:
+        os_ = _rows("out", out, H, D, q)
+        if out.shape[0] != rows:
+            raise ValueError(f"out: {rows} rows expected")
+    _launch(dev, stream, "nvq_attn_prefill", q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, dt,
+            _index("cu_q", cu_q, dev, B + 1), _index("cu_k", cu_k, dev, B + 1), B, rows, keys, H, Hk, D,
+            D ** -0.5 if scale is None else scale, 1 if causal else 0, out.data_ptr(), os_)
     return out
 
 

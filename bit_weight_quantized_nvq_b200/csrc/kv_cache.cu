@@ -21,7 +21,8 @@ namespace nvq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kElems = 8;      // values per thread: a quarter of a Q8_0 block
+constexpr int kElems = 16;     // values per thread: half a Q8_0 block
+constexpr int kMaxRows = kThreads / 32;
 
 __device__ unsigned int g_kv_error_flags = 0;   // bit 1: a bad index
 
@@ -30,7 +31,8 @@ struct Paged {
   const int32_t* cu;       // [B + 1]
   const int32_t* lens;     // [B]
   const int32_t* table;    // [B, max_pages]
-  int B, rows, max_pages, n_pages, page, heads, dim;
+  int B, rows, max_pages, n_pages, page, heads, dim_shift;
+  int per_row;             // threads of one row: its K, then its V
 };
 
 // (page * heads * page_size + offset), the token's place for head 0, or -1
@@ -40,26 +42,42 @@ __device__ __forceinline__ int64_t warp_place(const Paged& p, int row, int lane)
   const int b = dev::warp_find_seq(p.cu, p.B, row, lane);
   if (b >= p.B) return -1;
   const int64_t pos = static_cast<int64_t>(__ldg(p.lens + b)) - __ldg(p.cu + b + 1) + row;
-  int page = -1;
-  if (pos >= 0 && pos < static_cast<int64_t>(p.max_pages) * p.page)
-    page = __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + pos / p.page);
+  int page = -1, off = 0;
+  if (pos >= 0 && pos < static_cast<int64_t>(p.max_pages) * p.page) {
+    // below 2^47: an exact quotient needs 64 bits only for contexts over 2^31
+    const int col = pos <= INT32_MAX ? static_cast<int>(pos) / p.page : static_cast<int>(pos / p.page);
+    off = static_cast<int>(pos - static_cast<int64_t>(col) * p.page);
+    page = __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + col);
+  }
   if (page < 0 || page >= p.n_pages) {
     if (lane == 0) atomicOr(&g_kv_error_flags, 2u);
     return -1;
   }
-  return static_cast<int64_t>(page) * p.heads * p.page + pos % p.page;
+  return static_cast<int64_t>(page) * p.heads * p.page + off;
 }
 
-// One CTA per group of `rpc` rows (at most one row per warp): warp w finds
-// the place of row w, then every thread takes kElems values of K or V.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-kv_write_kernel(Paged p, int rpc, const T* __restrict__ k, int64_t k_stride,
-                const T* __restrict__ v, int64_t v_stride, int8_t* __restrict__ kc,
-                __half* __restrict__ ks, int8_t* __restrict__ vc, __half* __restrict__ vs) {
-  __shared__ int64_t place[kThreads / 32];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+// One CTA per `rpc` rows: warp w finds the place of row w, then thread t takes
+// the CTA's 16-value pieces t, t + 256, ..  A piece is in K or V of one row.
+struct Piece {
+  int64_t at;        // row's place (-1: none)
+  int64_t cached;    // its first value in the codes
+  int row, elem;     // packed row, first element of the row
+  bool is_v;
+};
+__device__ __forceinline__ Piece piece_of(const Paged& p, const int64_t* place, int row0, int t) {
+  Piece x;
+  const int r = t / p.per_row;
+  int e = t - r * p.per_row;
+  x.is_v = 2 * e >= p.per_row;
+  if (x.is_v) e -= p.per_row / 2;
+  x.row = row0 + r;
+  x.elem = e * kElems;
+  x.at = place[r];
+  const int h = x.elem >> p.dim_shift;
+  x.cached = ((x.at + static_cast<int64_t>(h) * p.page) << p.dim_shift) + (x.elem - (h << p.dim_shift));
+  return x;
+}
+__device__ __forceinline__ int find_places(const Paged& p, int rpc, int64_t* place) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row0 = blockIdx.x * rpc;
   if (warp < rpc) {
@@ -67,92 +85,107 @@ kv_write_kernel(Paged p, int rpc, const T* __restrict__ k, int64_t k_stride,
     if (lane == 0) place[warp] = at;
   }
   __syncthreads();
-  const int half_row = p.heads * p.dim / kElems;      // threads of one row's K
-  const int n = min(rpc, p.rows - row0) * 2 * half_row;
-  // n is a multiple of 16, so the four lanes of a block run together; the
-  // mask names only them
-  const unsigned quad = 0xFu << (lane & 28);
+  return min(rpc, p.rows - row0) * p.per_row;       // pieces
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+kv_write_kernel(const Paged p, int rpc, const T* __restrict__ k, int64_t k_stride,
+                const T* __restrict__ v, int64_t v_stride, int8_t* __restrict__ kc,
+                __half* __restrict__ ks, int8_t* __restrict__ vc, __half* __restrict__ vs) {
+  __shared__ int64_t place[kMaxRows];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n = find_places(p, rpc, place);
+  // n is even, so both lanes of a block run together; the mask names only them
+  const unsigned pair = 3u << (threadIdx.x & 30);
   for (int t = threadIdx.x; t < n; t += kThreads) {
-    const int r = t / (2 * half_row);
-    int e = t - r * 2 * half_row;
-    const bool is_v = e >= half_row;
-    if (is_v) e -= half_row;
-    const T* src = is_v ? v + (row0 + r) * v_stride : k + (row0 + r) * k_stride;
-    const auto in = *reinterpret_cast<const dev::Vec<T, kElems>*>(src + static_cast<int64_t>(e) * kElems);
-    float x[kElems], a = 0.0f;
+    const Piece x = piece_of(p, place, blockIdx.x * rpc, t);
+    const T* src = (x.is_v ? v + x.row * v_stride : k + x.row * k_stride) + x.elem;
+    const auto in = *reinterpret_cast<const dev::Vec<T, kElems>*>(src);
+    float f[kElems], a = 0.0f;
 #pragma unroll
     for (int i = 0; i < kElems; ++i) {
-      x[i] = dev::to_f32(in.v[i]);
-      a = fmaxf(a, fabsf(x[i]));
+      f[i] = dev::to_f32(in.v[i]);
+      a = fmaxf(a, fabsf(f[i]));
     }
-    a = fmaxf(a, __shfl_xor_sync(quad, a, 1));
-    a = fmaxf(a, __shfl_xor_sync(quad, a, 2));
+    a = fmaxf(a, __shfl_xor_sync(pair, a, 1));
     const float d32 = __fdiv_rn(a, 127.0f);
-    uint32_t w[2] = {0u, 0u};
+    uint32_t w[kElems / 4] = {};
     if (d32 > 0.0f) {
 #pragma unroll
       for (int i = 0; i < kElems; ++i) {
-        int q = __float2int_rn(__fdiv_rn(x[i], d32));
+        int q = __float2int_rn(__fdiv_rn(f[i], d32));
         q = max(-127, min(127, q));
         w[i >> 2] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * (i & 3));
       }
     }
-    const int64_t at = place[r];
-    if (at < 0) continue;
-    const int h = e * kElems / p.dim;
-    const int64_t o = (at + static_cast<int64_t>(h) * p.page) * p.dim + (e * kElems - h * p.dim);
-    *reinterpret_cast<uint2*>((is_v ? vc : kc) + o) = make_uint2(w[0], w[1]);
-    if ((lane & 3) == 0) (is_v ? vs : ks)[o / 32] = __float2half_rn(d32);
+    if (x.at < 0) continue;
+    *reinterpret_cast<uint4*>((x.is_v ? vc : kc) + x.cached) = make_uint4(w[0], w[1], w[2], w[3]);
+    if ((t & 1) == 0) (x.is_v ? vs : ks)[x.cached / 32] = __float2half_rn(d32);
   }
 }
 
 template <typename T>
+__device__ __forceinline__ void read_piece(const uint4 q, float d, T* dst) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  dev::Vec<T, kElems> out;
+#pragma unroll
+  for (int i = 0; i < kElems; ++i) {
+    // 0x4B0000bb is 2^23 + code + 128.  code * scale has at most 18
+    // significant bits: exact in fp32, rounded once
+    const uint32_t u = __byte_perm(w[i >> 2] ^ 0x80808080u, 0x4B000000u, 0x7440 + (i & 3));
+    out.v[i] = dev::from_f32<T>((__uint_as_float(u) - 8388736.0f) * d);
+  }
+  *reinterpret_cast<dev::Vec<T, kElems>*>(dst) = out;
+}
+
+template <typename T>
 __global__ void __launch_bounds__(kThreads)
-kv_read_kernel(Paged p, int rpc, const int8_t* __restrict__ kc, const __half* __restrict__ ks,
+kv_read_kernel(const Paged p, int rpc, const int8_t* __restrict__ kc, const __half* __restrict__ ks,
                const int8_t* __restrict__ vc, const __half* __restrict__ vs, T* __restrict__ k,
                int64_t k_stride, T* __restrict__ v, int64_t v_stride) {
-  __shared__ int64_t place[kThreads / 32];
+  __shared__ int64_t place[kMaxRows];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row0 = blockIdx.x * rpc;
-  if (warp < rpc) {
-    const int64_t at = row0 + warp < p.rows ? warp_place(p, row0 + warp, lane) : -1;
-    if (lane == 0) place[warp] = at;
-  }
-  __syncthreads();
-  const int half_row = p.heads * p.dim / kElems;
-  const int n = min(rpc, p.rows - row0) * 2 * half_row;
-  for (int t = threadIdx.x; t < n; t += kThreads) {
-    const int r = t / (2 * half_row);
-    int e = t - r * 2 * half_row;
-    const bool is_v = e >= half_row;
-    if (is_v) e -= half_row;
-    const int64_t at = place[r];
-    if (at < 0) continue;
-    const int h = e * kElems / p.dim;
-    const int64_t o = (at + static_cast<int64_t>(h) * p.page) * p.dim + (e * kElems - h * p.dim);
-    const auto q = *reinterpret_cast<const dev::Vec<int8_t, kElems>*>((is_v ? vc : kc) + o);
-    // code * scale has at most 18 significant bits: exact in fp32, rounded once
-    const float d = __half2float((is_v ? vs : ks)[o / 32]);
-    dev::Vec<T, kElems> out;
+  const int n = find_places(p, rpc, place);
+  // four pieces' loads in flight before the first is used
+  for (int t0 = threadIdx.x; t0 < n; t0 += 4 * kThreads) {
+    uint4 q[4];
+    __half d[4];
+    T* dst[4];
 #pragma unroll
-    for (int i = 0; i < kElems; ++i) out.v[i] = dev::from_f32<T>(static_cast<float>(q.v[i]) * d);
-    T* dst = is_v ? v + (row0 + r) * v_stride : k + (row0 + r) * k_stride;
-    *reinterpret_cast<dev::Vec<T, kElems>*>(dst + static_cast<int64_t>(e) * kElems) = out;
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + i * kThreads;
+      dst[i] = nullptr;
+      if (t < n) {
+        const Piece x = piece_of(p, place, blockIdx.x * rpc, t);
+        if (x.at >= 0) {
+          dst[i] = (x.is_v ? v + x.row * v_stride : k + x.row * k_stride) + x.elem;
+          q[i] = __ldcs(reinterpret_cast<const uint4*>((x.is_v ? vc : kc) + x.cached));
+          d[i] = (x.is_v ? vs : ks)[x.cached / 32];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (dst[i] != nullptr) read_piece(q[i], __half2float(d[i]), dst[i]);
   }
 }
 
 Paged paged_of(const nvq_kv_cache& c, const KvBatch& b) {
   return {b.cu_seqlens, b.seq_lens, b.block_table, static_cast<int>(b.B), static_cast<int>(b.rows),
           static_cast<int>(b.max_pages), static_cast<int>(c.n_pages), static_cast<int>(c.page_size),
-          static_cast<int>(c.n_kv_heads), static_cast<int>(c.head_dim)};
+          static_cast<int>(c.n_kv_heads), c.head_dim == 64 ? 6 : 7,
+          static_cast<int>(2 * c.n_kv_heads * c.head_dim / kElems)};
 }
 
-// rows per CTA: as many as fill its threads, at most one per warp
-int rows_per_cta(const nvq_kv_cache& c) {
-  const int64_t per_row = 2 * c.n_kv_heads * c.head_dim / kElems;
-  return static_cast<int>(per_row >= kThreads ? 1 : kThreads / per_row > 8 ? 8 : kThreads / per_row);
+// Rows per CTA, one per warp at most: the look-ups of a row's place are a
+// chain of four loads, so a CTA makes several at once, but few rows are
+// spread over the SMs.
+int rows_per_cta(const KvBatch& b) {
+  const int64_t r = b.rows / (4 * static_cast<int64_t>(device_sm_count()));
+  return static_cast<int>(r < 1 ? 1 : r > kMaxRows ? kMaxRows : r);
 }
 
 cudaLaunchConfig_t config(int64_t rows, int rpc, cudaStream_t stream, cudaLaunchAttribute* attr) {
@@ -171,7 +204,7 @@ template <typename T>
 cudaError_t write_t(const nvq_kv_cache& c, const KvBatch& b, const void* k, int64_t k_stride,
                     const void* v, int64_t v_stride, cudaStream_t stream) {
   cudaLaunchAttribute attr;
-  const int rpc = rows_per_cta(c);
+  const int rpc = rows_per_cta(b);
   const cudaLaunchConfig_t cfg = config(b.rows, rpc, stream, &attr);
   return cudaLaunchKernelEx(&cfg, kv_write_kernel<T>, paged_of(c, b), rpc, static_cast<const T*>(k),
                             k_stride, static_cast<const T*>(v), v_stride, c.k_codes,
@@ -183,7 +216,7 @@ template <typename T>
 cudaError_t read_t(const nvq_kv_cache& c, const KvBatch& b, void* k, int64_t k_stride, void* v,
                    int64_t v_stride, cudaStream_t stream) {
   cudaLaunchAttribute attr;
-  const int rpc = rows_per_cta(c);
+  const int rpc = rows_per_cta(b);
   const cudaLaunchConfig_t cfg = config(b.rows, rpc, stream, &attr);
   return cudaLaunchKernelEx(&cfg, kv_read_kernel<T>, paged_of(c, b), rpc,
                             static_cast<const int8_t*>(c.k_codes),
