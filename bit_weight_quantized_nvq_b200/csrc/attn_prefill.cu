@@ -76,7 +76,7 @@ struct Cfg {
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kOffRing = 2 * kBlock;
   static constexpr int kOffBars = kOffRing + kStages * kBlock;
-  static constexpr int kBars = 2 * kStages + 2 + 4 + 4 + 2 + 1;
+  static constexpr int kBars = 2 * kStages + 2 + 4 + 4 + 2 + 2 + 1;
   static constexpr int kOffMisc = kOffBars + 8 * kBars;
   static constexpr int kSmem = kOffMisc + 16 + 4 * kItemFlags + 1024;
 };
@@ -313,7 +313,8 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   auto s_full = [&](int s, int b) { return bar(2 * C::kStages + 2 + 2 * s + b); };
   auto p_full = [&](int s, int b) { return bar(2 * C::kStages + 6 + 2 * s + b); };
   auto o_done = [&](int s) { return bar(2 * C::kStages + 10 + s); };
-  const uint32_t mma_done = bar(2 * C::kStages + 12);
+  auto o_full = [&](int s) { return bar(2 * C::kStages + 12 + s); };
+  const uint32_t mma_done = bar(2 * C::kStages + 14);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* found = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);
@@ -332,6 +333,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         ptx::mbar_init(p_full(s, b), 4);
       }
       ptx::mbar_init(o_done(s), 1);
+      ptx::mbar_init(o_full(s), 1);
     }
     ptx::mbar_init(mma_done, 2);
     *abort_flag = 0;
@@ -460,7 +462,8 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
 #pragma unroll
           for (int e = 0; e < kStep / 16; ++e)
             ptx::mma_f16_ts(t_o, t_s + kStep * b + 8 * e, vd + ((e * 16 * 128) >> 4), idesc_o, i > 0 || e > 0);
-          ptx::mma_commit(o_done(s));
+          ptx::mma_commit(o_done(s));                       // every step, and
+          if (i + 1 == steps) ptx::mma_commit(o_full(s));   // every item
           if (b || i + 1 == steps) ptx::mma_commit(kv_empty(v % C::kStages));
         }
         __syncwarp();
@@ -489,7 +492,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
     const float c = a.scale_log2;
     int g = 0, items = 0;
     uint32_t s_par = 0;                            // parity of each buffer's next S
-    int sent = 0;                                  // steps handed on, over all items
+    int sent = 0, o_count = 0;                     // steps handed on, results taken, over all items
     bool ok = true;
     Item it;
     for (int t = 0, x; ok && (x = item_of(t), t * static_cast<int>(gridDim.x) < a.max_items); ++t) {
@@ -610,10 +613,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       // -------- the tile's results
       const bool some = steps > 0;
       if (some) {
-        // the last two products, one after the other: a parity tells only two
-        // phases apart
-        if (steps > 1) ok = warp_wait(o_done(s), (sent - 2) & 1);
-        ok = ok && warp_wait(o_done(s), (sent - 1) & 1);
+        ok = warp_wait(o_full(s), o_count++ & 1);
         if (!ok) break;
         ptx::tc_fence_after();
       }

@@ -12,6 +12,8 @@
 //
 // Both kernels are HBM-bound when they move many rows (write: e + 1.0625
 // bytes per value, read: 1.0625 + e) and launch-bound for a decode step.
+#include <cstring>
+
 #include <cuda_fp16.h>
 
 #include "kv_device.cuh"
@@ -21,8 +23,7 @@ namespace nvq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kElems = 16;     // values per thread: half a Q8_0 block
-constexpr int kMaxRows = kThreads / 32;
+constexpr int kBatch = 4;      // pieces of a lane whose loads are in flight together
 
 __device__ unsigned int g_kv_error_flags = 0;   // bit 1: a bad index
 
@@ -32,7 +33,7 @@ struct Paged {
   const int32_t* lens;     // [B]
   const int32_t* table;    // [B, max_pages]
   int B, rows, max_pages, n_pages, page, heads, dim_shift;
-  int per_row;             // threads of one row: its K, then its V
+  int parts;               // warps that share a row
 };
 
 // (page * heads * page_size + offset), the token's place for head 0, or -1
@@ -44,9 +45,8 @@ __device__ __forceinline__ int64_t warp_place(const Paged& p, int row, int lane)
   const int64_t pos = static_cast<int64_t>(__ldg(p.lens + b)) - __ldg(p.cu + b + 1) + row;
   int page = -1, off = 0;
   if (pos >= 0 && pos < static_cast<int64_t>(p.max_pages) * p.page) {
-    // below 2^47: an exact quotient needs 64 bits only for contexts over 2^31
-    const int col = pos <= INT32_MAX ? static_cast<int>(pos) / p.page : static_cast<int>(pos / p.page);
-    off = static_cast<int>(pos - static_cast<int64_t>(col) * p.page);
+    const int col = static_cast<int>(static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page));   // a length is below 2^31
+    off = static_cast<int>(pos) - col * p.page;
     page = __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + col);
   }
   if (page < 0 || page >= p.n_pages) {
@@ -56,143 +56,185 @@ __device__ __forceinline__ int64_t warp_place(const Paged& p, int row, int lane)
   return static_cast<int64_t>(page) * p.heads * p.page + off;
 }
 
-// One CTA per `rpc` rows: warp w finds the place of row w, then thread t takes
-// the CTA's 16-value pieces t, t + 256, ..  A piece is in K or V of one row.
-struct Piece {
-  int64_t at;        // row's place (-1: none)
-  int64_t cached;    // its first value in the codes
-  int row, elem;     // packed row, first element of the row
-  bool is_v;
-};
-__device__ __forceinline__ Piece piece_of(const Paged& p, const int64_t* place, int row0, int t) {
-  Piece x;
-  const int r = t / p.per_row;
-  int e = t - r * p.per_row;
-  x.is_v = 2 * e >= p.per_row;
-  if (x.is_v) e -= p.per_row / 2;
-  x.row = row0 + r;
-  x.elem = e * kElems;
-  x.at = place[r];
-  const int h = x.elem >> p.dim_shift;
-  x.cached = ((x.at + static_cast<int64_t>(h) * p.page) << p.dim_shift) + (x.elem - (h << p.dim_shift));
-  return x;
-}
-__device__ __forceinline__ int find_places(const Paged& p, int rpc, int64_t* place) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row0 = blockIdx.x * rpc;
-  if (warp < rpc) {
-    const int64_t at = row0 + warp < p.rows ? warp_place(p, row0 + warp, lane) : -1;
-    if (lane == 0) place[warp] = at;
+// A warp's share of a row: the 16-byte pieces of the packed side (4 or 8
+// values) lane, lane + 32, .. of K and then of V, so that both sides are
+// read and written in whole lines.  The look-up of the row's place is a
+// chain of four loads, hidden by the other warps.
+template <typename T>
+struct Share {
+  static constexpr int kElems = 16 / sizeof(T);
+  int row, e0, e1;         // elements of K and V of the row: e0 .. e1 - 1
+  int64_t at;
+  __device__ __forceinline__ bool find(const Paged& p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    row = static_cast<int>(w / p.parts);
+    if (row >= p.rows) return false;
+    const int part = static_cast<int>(w - static_cast<int64_t>(row) * p.parts);
+    // shares are whole warps' pieces (the width is a multiple of 64)
+    const int pieces = (p.heads << p.dim_shift) / kElems;
+    const int each = (pieces + 32 * p.parts - 1) / (32 * p.parts) * 32;
+    e0 = min(part * each, pieces) * kElems;
+    e1 = min((part + 1) * each, pieces) * kElems;
+    at = warp_place(p, row, lane);
+    return at >= 0;
   }
-  __syncthreads();
-  return min(rpc, p.rows - row0) * p.per_row;       // pieces
+  // the first code of the piece that starts at element e
+  __device__ __forceinline__ int64_t code(const Paged& p, int e) const {
+    const int h = e >> p.dim_shift;
+    return ((at + static_cast<int64_t>(h) * p.page) << p.dim_shift) + (e - (h << p.dim_shift));
+  }
+};
+// kElems codes as one word or two.
+template <int N> struct Codes;
+template <> struct Codes<4> { using type = uint32_t; };
+template <> struct Codes<8> { using type = uint2; };
+
+// Codes of N values with scale d32, rint(x / d32) of the correctly rounded
+// quotient: x * (1 / d32) is within 2^-22 of it, relatively, and below 128, so
+// where it is not within 2^-14 of a tie it rounds to the same number; else,
+// and where the reciprocal may leave the normal range, by the division itself.
+// Adding 1.5 * 2^23 rounds to the nearest even whole number and leaves it in
+// the low bits, which spares the conversion units.
+template <int N>
+__device__ __forceinline__ void quantise(const float (&f)[N], float d32, uint32_t (&w)[N / 4]) {
+  constexpr float kRound = 12582912.0f;
+  const float inv = __frcp_rn(d32);
+  bool exact = !(d32 >= 0x1p-100f && d32 <= 0x1p100f);
+  uint32_t q[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float t = f[i] * inv, u = t + kRound;
+    exact |= fabsf(t - (u - kRound)) > 0.5f - 0x1p-14f;
+    q[i] = __float_as_uint(u);
+  }
+  if (exact) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = max(-127, min(127, __float2int_rn(__fdiv_rn(f[i], d32))));
+  }
+#pragma unroll
+  for (int i = 0; i < N; i += 4)
+    w[i / 4] = __byte_perm(__byte_perm(q[i], q[i + 1], 0x0040), __byte_perm(q[i + 2], q[i + 3], 0x0040), 0x5410);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-kv_write_kernel(const Paged p, int rpc, const T* __restrict__ k, int64_t k_stride,
+kv_write_kernel(const Paged p, const T* __restrict__ k, int64_t k_stride,
                 const T* __restrict__ v, int64_t v_stride, int8_t* __restrict__ kc,
                 __half* __restrict__ ks, int8_t* __restrict__ vc, __half* __restrict__ vs) {
-  __shared__ int64_t place[kMaxRows];
+  constexpr int N = Share<T>::kElems, kLanes = 32 / N;      // lanes of a Q8_0 block
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n = find_places(p, rpc, place);
-  // n is even, so both lanes of a block run together; the mask names only them
-  const unsigned pair = 3u << (threadIdx.x & 30);
-  for (int t = threadIdx.x; t < n; t += kThreads) {
-    const Piece x = piece_of(p, place, blockIdx.x * rpc, t);
-    const T* src = (x.is_v ? v + x.row * v_stride : k + x.row * k_stride) + x.elem;
-    const auto in = *reinterpret_cast<const dev::Vec<T, kElems>*>(src);
-    float f[kElems], a = 0.0f;
+  Share<T> x;
+  if (!x.find(p)) return;                 // whole warps leave together
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < kElems; ++i) {
-      f[i] = dev::to_f32(in.v[i]);
-      a = fmaxf(a, fabsf(f[i]));
-    }
-    a = fmaxf(a, __shfl_xor_sync(pair, a, 1));
-    const float d32 = __fdiv_rn(a, 127.0f);
-    uint32_t w[kElems / 4] = {};
-    if (d32 > 0.0f) {
+  for (int is_v = 0; is_v < 2; ++is_v) {
+    const T* src = is_v ? v + x.row * v_stride : k + x.row * k_stride;
+    int8_t* codes = is_v ? vc : kc;
+    __half* scales = is_v ? vs : ks;
+    for (int e0 = x.e0 + lane * N; e0 - lane * N < x.e1; e0 += kBatch * 32 * N) {
+      dev::Vec<T, N> in[kBatch];
 #pragma unroll
-      for (int i = 0; i < kElems; ++i) {
-        int q = __float2int_rn(__fdiv_rn(f[i], d32));
-        q = max(-127, min(127, q));
-        w[i >> 2] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * (i & 3));
+      for (int i = 0; i < kBatch; ++i) {
+        const int e = e0 + i * 32 * N;
+        if (e < x.e1) in[i] = *reinterpret_cast<const dev::Vec<T, N>*>(src + e);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int e = e0 + i * 32 * N;
+        // the lanes of a block are inside the share together
+        const unsigned mask = __ballot_sync(0xffffffffu, e < x.e1);
+        if (e >= x.e1) continue;
+        float f[N], a = 0.0f;
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+          f[u] = dev::to_f32(in[i].v[u]);
+          a = fmaxf(a, fabsf(f[u]));
+        }
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o));
+        const float d32 = __fdiv_rn(a, 127.0f);
+        uint32_t w[N / 4] = {};
+        if (d32 > 0.0f) quantise<N>(f, d32, w);
+        const int64_t at = x.code(p, e);
+        typename Codes<N>::type word;
+        memcpy(&word, w, sizeof(w));
+        *reinterpret_cast<typename Codes<N>::type*>(codes + at) = word;
+        if (lane % kLanes == 0) scales[at / 32] = __float2half_rn(d32);
       }
     }
-    if (x.at < 0) continue;
-    *reinterpret_cast<uint4*>((x.is_v ? vc : kc) + x.cached) = make_uint4(w[0], w[1], w[2], w[3]);
-    if ((t & 1) == 0) (x.is_v ? vs : ks)[x.cached / 32] = __float2half_rn(d32);
   }
-}
-
-template <typename T>
-__device__ __forceinline__ void read_piece(const uint4 q, float d, T* dst) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  dev::Vec<T, kElems> out;
-#pragma unroll
-  for (int i = 0; i < kElems; ++i) {
-    // 0x4B0000bb is 2^23 + code + 128.  code * scale has at most 18
-    // significant bits: exact in fp32, rounded once
-    const uint32_t u = __byte_perm(w[i >> 2] ^ 0x80808080u, 0x4B000000u, 0x7440 + (i & 3));
-    out.v[i] = dev::from_f32<T>((__uint_as_float(u) - 8388736.0f) * d);
-  }
-  *reinterpret_cast<dev::Vec<T, kElems>*>(dst) = out;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-kv_read_kernel(const Paged p, int rpc, const int8_t* __restrict__ kc, const __half* __restrict__ ks,
+kv_read_kernel(const Paged p, const int8_t* __restrict__ kc, const __half* __restrict__ ks,
                const int8_t* __restrict__ vc, const __half* __restrict__ vs, T* __restrict__ k,
                int64_t k_stride, T* __restrict__ v, int64_t v_stride) {
-  __shared__ int64_t place[kMaxRows];
+  constexpr int N = Share<T>::kElems;
+  using Word = typename Codes<N>::type;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n = find_places(p, rpc, place);
-  // four pieces' loads in flight before the first is used
-  for (int t0 = threadIdx.x; t0 < n; t0 += 4 * kThreads) {
-    uint4 q[4];
-    __half d[4];
-    T* dst[4];
+  Share<T> x;
+  if (!x.find(p)) return;
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = t0 + i * kThreads;
-      dst[i] = nullptr;
-      if (t < n) {
-        const Piece x = piece_of(p, place, blockIdx.x * rpc, t);
-        if (x.at >= 0) {
-          dst[i] = (x.is_v ? v + x.row * v_stride : k + x.row * k_stride) + x.elem;
-          q[i] = __ldcs(reinterpret_cast<const uint4*>((x.is_v ? vc : kc) + x.cached));
-          d[i] = (x.is_v ? vs : ks)[x.cached / 32];
+  for (int is_v = 0; is_v < 2; ++is_v) {
+    T* dst = is_v ? v + x.row * v_stride : k + x.row * k_stride;
+    const int8_t* codes = is_v ? vc : kc;
+    const __half* scales = is_v ? vs : ks;
+    for (int e0 = x.e0 + lane * N; e0 < x.e1; e0 += kBatch * 32 * N) {
+      Word q[kBatch];
+      __half d[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int e = e0 + i * 32 * N;
+        if (e < x.e1) {
+          const int64_t at = x.code(p, e);
+          q[i] = __ldcs(reinterpret_cast<const Word*>(codes + at));
+          d[i] = __ldg(scales + at / 32);
         }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (dst[i] != nullptr) read_piece(q[i], __half2float(d[i]), dst[i]);
+      for (int i = 0; i < kBatch; ++i) {
+        const int e = e0 + i * 32 * N;
+        if (e >= x.e1) continue;
+        uint32_t w[N / 4];
+        memcpy(w, &q[i], sizeof(w));
+        const float scale = __half2float(d[i]);
+        dev::Vec<T, N> out;
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+          // 0x4B0000bb is 2^23 + code + 128.  code * scale has at most 18
+          // significant bits: exact in fp32, rounded once
+          const uint32_t b = __byte_perm(w[u / 4] ^ 0x80808080u, 0x4B000000u, 0x7440 + (u % 4));
+          out.v[u] = dev::from_f32<T>((__uint_as_float(b) - 8388736.0f) * scale);
+        }
+        *reinterpret_cast<dev::Vec<T, N>*>(dst + e) = out;
+      }
+    }
   }
 }
 
-Paged paged_of(const nvq_kv_cache& c, const KvBatch& b) {
+// Warps that share a row: one where there are rows enough to fill the SMs (48
+// warps each), more for a decode step's few rows, as far as a warp still has
+// a piece of K and of V for each of its lanes.
+Paged paged_of(const nvq_kv_cache& c, const KvBatch& b, int elems) {
+  const int64_t width = c.n_kv_heads * c.head_dim;
+  int parts = 1;
+  while (b.rows * parts < 48 * static_cast<int64_t>(device_sm_count()) && 32 * elems * 2 * parts <= width) parts *= 2;
   return {b.cu_seqlens, b.seq_lens, b.block_table, static_cast<int>(b.B), static_cast<int>(b.rows),
           static_cast<int>(b.max_pages), static_cast<int>(c.n_pages), static_cast<int>(c.page_size),
-          static_cast<int>(c.n_kv_heads), c.head_dim == 64 ? 6 : 7,
-          static_cast<int>(2 * c.n_kv_heads * c.head_dim / kElems)};
+          static_cast<int>(c.n_kv_heads), c.head_dim == 64 ? 6 : 7, parts};
 }
 
-// Rows per CTA, one per warp at most: the look-ups of a row's place are a
-// chain of four loads, so a CTA makes several at once, but few rows are
-// spread over the SMs.
-int rows_per_cta(const KvBatch& b) {
-  const int64_t r = b.rows / (4 * static_cast<int64_t>(device_sm_count()));
-  return static_cast<int>(r < 1 ? 1 : r > kMaxRows ? kMaxRows : r);
-}
-
-cudaLaunchConfig_t config(int64_t rows, int rpc, cudaStream_t stream, cudaLaunchAttribute* attr) {
+cudaLaunchConfig_t config(const Paged& p, cudaStream_t stream, cudaLaunchAttribute* attr) {
   attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr->val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + rpc - 1) / rpc));
+  const int64_t warps = static_cast<int64_t>(p.rows) * p.parts;
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -204,9 +246,9 @@ template <typename T>
 cudaError_t write_t(const nvq_kv_cache& c, const KvBatch& b, const void* k, int64_t k_stride,
                     const void* v, int64_t v_stride, cudaStream_t stream) {
   cudaLaunchAttribute attr;
-  const int rpc = rows_per_cta(b);
-  const cudaLaunchConfig_t cfg = config(b.rows, rpc, stream, &attr);
-  return cudaLaunchKernelEx(&cfg, kv_write_kernel<T>, paged_of(c, b), rpc, static_cast<const T*>(k),
+  const Paged p = paged_of(c, b, 16 / sizeof(T));
+  const cudaLaunchConfig_t cfg = config(p, stream, &attr);
+  return cudaLaunchKernelEx(&cfg, kv_write_kernel<T>, p, static_cast<const T*>(k),
                             k_stride, static_cast<const T*>(v), v_stride, c.k_codes,
                             reinterpret_cast<__half*>(c.k_scales), c.v_codes,
                             reinterpret_cast<__half*>(c.v_scales));
@@ -216,10 +258,9 @@ template <typename T>
 cudaError_t read_t(const nvq_kv_cache& c, const KvBatch& b, void* k, int64_t k_stride, void* v,
                    int64_t v_stride, cudaStream_t stream) {
   cudaLaunchAttribute attr;
-  const int rpc = rows_per_cta(b);
-  const cudaLaunchConfig_t cfg = config(b.rows, rpc, stream, &attr);
-  return cudaLaunchKernelEx(&cfg, kv_read_kernel<T>, paged_of(c, b), rpc,
-                            static_cast<const int8_t*>(c.k_codes),
+  const Paged p = paged_of(c, b, 16 / sizeof(T));
+  const cudaLaunchConfig_t cfg = config(p, stream, &attr);
+  return cudaLaunchKernelEx(&cfg, kv_read_kernel<T>, p, static_cast<const int8_t*>(c.k_codes),
                             reinterpret_cast<const __half*>(c.k_scales),
                             static_cast<const int8_t*>(c.v_codes),
                             reinterpret_cast<const __half*>(c.v_scales), static_cast<T*>(k),
