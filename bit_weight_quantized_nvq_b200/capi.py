@@ -342,6 +342,11 @@ def debug_subblock_sums(codes: torch.Tensor, scales: torch.Tensor, g: float, q: 
 
 #: NVQ_F32, NVQ_F16, NVQ_BF16
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_I8, _I32, _F16 = torch.int8, torch.int32, torch.float16
+_HERE = nullcontext()
+
+# The checks below run before every launch of a decode step, so they compare
+# device numbers (-1: not a CUDA device) and whole shapes.
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -351,60 +356,57 @@ def _dtype(t: torch.Tensor) -> int:
     return code
 
 
-def _rows(name: str, t: torch.Tensor, heads: int, dim: int, like: torch.Tensor) -> int:
+def _rows(name: str, t: torch.Tensor, shape: tuple, like: torch.Tensor, dev: int) -> int:
     """Elements between the rows of t [rows, heads, dim], whose rows must be
-    contiguous; on the device and of the type of `like`."""
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
-        raise ValueError(f"{name}: [rows, {heads}, {dim}] expected, not {tuple(shape)}")
-    if t.device != like.device or t.dtype != like.dtype:
-        raise ValueError(f"{name}: {like.dtype} on {like.device} expected")
-    width = heads * dim
-    if t.is_contiguous():
-        return width
-    strides = t.stride()
-    if strides[2] != 1 or (heads > 1 and strides[1] != dim):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return strides[0] if shape[0] > 1 else width
-
-
-def _index(name: str, t: torch.Tensor, dev: torch.device, *shape: int) -> int:
-    if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous int32 on {dev} expected")
+    contiguous; of the given shape, on device `dev` and of the type of `like`."""
     if t.shape != shape:
         raise ValueError(f"{name}: shape {shape} expected, not {tuple(t.shape)}")
+    if t.get_device() != dev or t.dtype is not like.dtype:
+        raise ValueError(f"{name}: {like.dtype} on {like.device} expected")
+    if t.is_contiguous():
+        return shape[1] * shape[2]
+    strides = t.stride()
+    if strides[2] != 1 or (shape[1] > 1 and strides[1] != shape[2]):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return strides[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _index(name: str, t: torch.Tensor, dev: int, shape: tuple) -> int:
+    if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name}: contiguous int32 {shape} on device {dev} expected, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _cache(cache, dev: torch.device) -> KVCache:
+def _cache(cache, dev: int) -> KVCache:
     """The C descriptor of (k_codes, k_scales, v_codes, v_scales)."""
     kc, ks, vc, vs = cache
     shape = kc.shape
-    if len(shape) != 4 or vc.shape != shape or ks.shape != vs.shape \
-            or ks.shape != (shape[0], shape[1], shape[2], shape[3] // 32):
+    if len(shape) != 4:
+        raise ValueError("cache: codes [pages, kv_heads, page_size, head_dim] expected")
+    n, h, p, d = shape
+    scales = (n, h, p, d // 32)
+    if vc.shape != shape or ks.shape != scales or vs.shape != scales:
         raise ValueError("cache: keys and values as codes [pages, kv_heads, page_size, head_dim] "
                          "and scales [pages, kv_heads, page_size, head_dim / 32] expected")
-    for codes, scales in ((kc, ks), (vc, vs)):
-        if codes.dtype != torch.int8 or scales.dtype != torch.float16 or codes.device != dev \
-                or scales.device != dev or not codes.is_contiguous() or not scales.is_contiguous():
-            raise ValueError(f"cache: contiguous int8 codes and float16 scales on {dev} expected")
-    return KVCache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), *shape)
+    if not (kc.dtype is _I8 and vc.dtype is _I8 and ks.dtype is _F16 and vs.dtype is _F16
+            and kc.get_device() == dev and ks.get_device() == dev and vc.get_device() == dev
+            and vs.get_device() == dev and kc.is_contiguous() and ks.is_contiguous()
+            and vc.is_contiguous() and vs.is_contiguous()):
+        raise ValueError(f"cache: contiguous int8 codes and float16 scales on device {dev} expected")
+    return KVCache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), n, h, p, d)
 
 
-def _launch(dev: torch.device, stream, name: str, *args) -> None:
-    """Call an entry point with `dev` current, on its current stream unless
-    another is given."""
-    if dev.type != "cuda":
-        raise ValueError(f"{name}: tensors on a CUDA device expected, not {dev}")
-    if dev.index != torch.cuda.current_device():
+def _launch(dev: int, stream, name: str, fn, *args) -> None:
+    """Call an entry point with device `dev` current, on its current stream
+    unless another is given."""
+    if dev < 0:
+        raise ValueError(f"{name}: tensors on a CUDA device expected")
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            _check(name, getattr(_lib, name)(*args, _stream(stream)))
+            _check(name, fn(*args, _stream(stream)))
         return
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev.index)
-    else:
-        stream = _stream(stream)
-    status = getattr(_lib, name)(*args, stream)
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if status != NVQ_OK:
         raise NVQError(name, status)
 
@@ -426,16 +428,15 @@ def kv_write(cache, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
     or bfloat16; packed by sequence, the last positions of each) into the
     cache's pages (nvq_kv_write).  cu_seqlens int32 [B + 1], seq_lens int32
     [B] (these rows included), block_table int32 [B, max_pages]."""
-    dt, dev = _dtype(k), k.device
+    dt, dev = _dtype(k), k.get_device()
     c = _cache(cache, dev)
-    heads, dim, rows = c.n_kv_heads, c.head_dim, k.shape[0]
-    ks, vs = _rows("k", k, heads, dim, k), _rows("v", v, heads, dim, k)
-    if v.shape[0] != rows:
-        raise ValueError("v: as many rows as k expected")
+    rows = k.shape[0]
+    shape = (rows, c.n_kv_heads, c.head_dim)
+    ks, vs = _rows("k", k, shape, k, dev), _rows("v", v, shape, k, dev)
     B, cols = seq_lens.shape[0], block_table.shape[-1]
-    _launch(dev, stream, "nvq_kv_write", c, k.data_ptr(), ks, v.data_ptr(), vs, dt,
-            _index("cu_seqlens", cu_seqlens, dev, B + 1), _index("seq_lens", seq_lens, dev, B),
-            _index("block_table", block_table, dev, B, cols), B, cols, rows)
+    _launch(dev, stream, "nvq_kv_write", _lib.nvq_kv_write, c, k.data_ptr(), ks, v.data_ptr(), vs, dt,
+            _index("cu_seqlens", cu_seqlens, dev, (B + 1,)), _index("seq_lens", seq_lens, dev, (B,)),
+            _index("block_table", block_table, dev, (B, cols)), B, cols, rows)
 
 
 def kv_read(cache, cu_seqlens: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
@@ -445,21 +446,19 @@ def kv_read(cache, cu_seqlens: torch.Tensor, seq_lens: torch.Tensor, block_table
     cu_seqlens[b] positions of each sequence, packed; returns (k, v) of
     [rows, n_kv_heads, head_dim].  rows >= cu_seqlens[B]; rows behind the
     last sequence are left as they were."""
-    dev = cache[0].device
+    dev = cache[0].get_device()
     c = _cache(cache, dev)
-    heads, dim = c.n_kv_heads, c.head_dim
+    shape = (rows, c.n_kv_heads, c.head_dim)
     if k is None:
-        k = torch.empty((rows, heads, dim), dtype=dtype, device=dev)
+        k = cache[0].new_empty(shape, dtype=dtype)
     if v is None:
-        v = torch.empty((rows, heads, dim), dtype=k.dtype, device=dev)
+        v = k.new_empty(shape)
     dt = _dtype(k)
-    ks, vs = _rows("k", k, heads, dim, k), _rows("v", v, heads, dim, k)
-    if k.shape[0] != rows or v.shape[0] != rows or k.device != dev:
-        raise ValueError(f"k, v: {rows} rows on {dev} expected")
+    ks, vs = _rows("k", k, shape, k, dev), _rows("v", v, shape, k, dev)
     B, cols = seq_lens.shape[0], block_table.shape[-1]
-    _launch(dev, stream, "nvq_kv_read", c, k.data_ptr(), ks, v.data_ptr(), vs, dt,
-            _index("cu_seqlens", cu_seqlens, dev, B + 1), _index("seq_lens", seq_lens, dev, B),
-            _index("block_table", block_table, dev, B, cols), B, cols, rows)
+    _launch(dev, stream, "nvq_kv_read", _lib.nvq_kv_read, c, k.data_ptr(), ks, v.data_ptr(), vs, dt,
+            _index("cu_seqlens", cu_seqlens, dev, (B + 1,)), _index("seq_lens", seq_lens, dev, (B,)),
+            _index("block_table", block_table, dev, (B, cols)), B, cols, rows)
     return k, v
 
 
@@ -472,31 +471,28 @@ def attn_decode(cache, q: torch.Tensor, seq_lens: torch.Tensor, block_table: tor
     returns out of q's shape and type.  counters: device int32
     [B * n_heads], zero before the first call, left zero; calls that may
     overlap need their own.  scale: 1/sqrt(head_dim) unless given."""
-    dt, dev = _dtype(q), q.device
+    dt, dev = _dtype(q), q.get_device()
     c = _cache(cache, dev)
     B, cols = seq_lens.shape[0], block_table.shape[-1]
     H, D = q.shape[1], c.head_dim
-    qs = _rows("q", q, H, D, q)
-    if q.shape[0] != B:
-        raise ValueError(f"q: {B} rows expected, one per sequence")
-    if counters.dtype != torch.int32 or counters.device != dev or not counters.is_contiguous() \
+    shape = (B, H, D)
+    qs = _rows("q", q, shape, q, dev)
+    if counters.dtype is not _I32 or counters.get_device() != dev or not counters.is_contiguous() \
             or counters.numel() < B * H:
-        raise ValueError(f"counters: contiguous int32 [{B * H}] on {dev} expected")
+        raise ValueError(f"counters: contiguous int32 [{B * H}] on device {dev} expected")
     if out is None:
-        out = torch.empty((B, H, D), dtype=q.dtype, device=dev)
+        out = q.new_empty(shape)
         os_ = H * D
     else:
-        os_ = _rows("out", out, H, D, q)
-        if out.shape[0] != B:
-            raise ValueError(f"out: {B} rows expected")
+        os_ = _rows("out", out, shape, q, dev)
     if workspace is None:
-        if dev.type != "cuda":
-            raise ValueError(f"nvq_attn_decode: tensors on a CUDA device expected, not {dev}")
-        with torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else nullcontext():
+        if dev < 0:
+            raise ValueError("nvq_attn_decode: tensors on a CUDA device expected")
+        with torch.cuda.device(dev) if dev != torch._C._cuda_getDevice() else _HERE:
             nbytes = _lib.nvq_attn_decode_workspace_size(B, H, c.n_kv_heads, D)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-    _launch(dev, stream, "nvq_attn_decode", c, q.data_ptr(), qs, dt,
-            _index("seq_lens", seq_lens, dev, B), _index("block_table", block_table, dev, B, cols),
+        workspace = q.new_empty(max(nbytes, 16), dtype=torch.uint8)
+    _launch(dev, stream, "nvq_attn_decode", _lib.nvq_attn_decode, c, q.data_ptr(), qs, dt,
+            _index("seq_lens", seq_lens, dev, (B,)), _index("block_table", block_table, dev, (B, cols)),
             B, cols, H, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
             counters.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
@@ -510,27 +506,25 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.
     head_dim], k and v [total_k, n_kv_heads, head_dim], float16 or bfloat16;
     cu_q, cu_k int32 [B + 1] (cu_k: cu_q unless given); returns out of q's
     shape and type, rows from cu_q[B] on left as they were."""
-    dt, dev = _dtype(q), q.device
+    dt, dev = _dtype(q), q.get_device()
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k: [rows, heads, head_dim] expected")
-    rows, H, D = q.shape
+    rows, H, D = shape = q.shape
     keys, Hk = k.shape[0], k.shape[1]
     if cu_k is None:
         cu_k = cu_q
-    qs, ks, vs = _rows("q", q, H, D, q), _rows("k", k, Hk, D, q), _rows("v", v, Hk, D, q)
-    if v.shape[0] != keys:
-        raise ValueError("v: as many rows as k expected")
+    qs = _rows("q", q, shape, q, dev)
+    ks, vs = _rows("k", k, (keys, Hk, D), q, dev), _rows("v", v, (keys, Hk, D), q, dev)
     B = cu_q.shape[0] - 1
     if out is None:
-        out = torch.empty((rows, H, D), dtype=q.dtype, device=dev)
+        out = q.new_empty(shape)
         os_ = H * D
     else:
-        os_ = _rows("out", out, H, D, q)
-        if out.shape[0] != rows:
-            raise ValueError(f"out: {rows} rows expected")
-    _launch(dev, stream, "nvq_attn_prefill", q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, dt,
-            _index("cu_q", cu_q, dev, B + 1), _index("cu_k", cu_k, dev, B + 1), B, rows, keys, H, Hk, D,
-            D ** -0.5 if scale is None else scale, 1 if causal else 0, out.data_ptr(), os_)
+        os_ = _rows("out", out, shape, q, dev)
+    _launch(dev, stream, "nvq_attn_prefill", _lib.nvq_attn_prefill, q.data_ptr(), qs, k.data_ptr(), ks,
+            v.data_ptr(), vs, dt, _index("cu_q", cu_q, dev, (B + 1,)), _index("cu_k", cu_k, dev, (B + 1,)),
+            B, rows, keys, H, Hk, D, D ** -0.5 if scale is None else scale, 1 if causal else 0,
+            out.data_ptr(), os_)
     return out
 
 

@@ -57,6 +57,7 @@ constexpr int kTile = 64;            // tokens of a tile
 constexpr int kWarps = 4;            // 16 tokens of a tile each
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnitCost = 3;         // a unit's start and end, in tiles
+constexpr int kFlush = 4;            // tiles between additions of the accumulators, with fp32
 constexpr float kLazy = 8.0f;        // the running maximum may lag by this power of two
 
 // How the 16 rows of an MMA are used: fp32 heads as hi (rows 0-7) and lo
@@ -85,7 +86,7 @@ template <int D, Rows R>
 struct Cfg {
   static constexpr int kHeads = R == kTwo ? 16 : 8;          // heads of a chunk
   static constexpr int kBlocks = D / 32;
-  static constexpr int kStages = 4;
+  static constexpr int kStages = R == kSplit ? 6 : 4;
   static constexpr int kCodes = 16 * D;                      // bytes of 16 tokens' codes
   static constexpr int kScales = 16 * kBlocks * 2;
   static constexpr int kStage = 2 * kCodes + 2 * kScales;    // K, V, scales of K, of V
@@ -93,7 +94,7 @@ struct Cfg {
   static constexpr int kPart = D + 4;                        // floats of a part's row: o, m, l
   static constexpr int kOffMl = kWarps * kRing;
   static constexpr int kSmem = kOffMl + kWarps * kHeads * 8;
-  static constexpr int kCtas = R == kTwo ? 2 : 3;            // per SM
+  static constexpr int kCtas = R == kOne ? 3 : 2;            // per SM
 };
 
 // The work in order: sequence by sequence, unit by unit, each as kUnitCost
@@ -548,7 +549,20 @@ attn_decode_kernel(const DecodeArgs a) {
 #pragma unroll
     for (int h = 0; h < kH; ++h) m[h] = -INFINITY, l[h] = 0.0f;
 
+    // The tensor core adds to its accumulators by truncation, so with fp32 they
+    // hold kFlush tiles at a time and are added up here (131072 tokens: 2.6e-6
+    // of error without it).
+    float sum[R == kSplit ? D / 16 : 1][4] = {};
     for (int t = n_here; t > 0; --t, rem -= kTile) {
+      if (R == kSplit && (n_here - t) % kFlush == kFlush - 1) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            sum[i % (R == kSplit ? D / 16 : 1)][u] += o[0][i][u];
+            o[0][i][u] = 0.0f;
+          }
+      }
       issue();                                  // into the slot of the tile before
       ptx::cp_async_wait<C::kStages - 1>();
       __syncwarp();
@@ -628,7 +642,10 @@ attn_decode_kernel(const DecodeArgs a) {
             // the factors of the heads whose sums this lane holds
             const float c0 = __shfl_sync(0xffffffffu, c, 8 * j), c1 = __shfl_sync(0xffffffffu, c, 8 * j + 4);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) o[h][i][0] *= c0, o[h][i][1] *= c1, o[h][i][2] *= c0, o[h][i][3] *= c1;
+            for (int i = 0; i < D / 16; ++i) {
+              o[h][i][0] *= c0, o[h][i][1] *= c1, o[h][i][2] *= c0, o[h][i][3] *= c1;
+              if constexpr (R == kSplit) sum[i][0] *= c0, sum[i][1] *= c1, sum[i][2] *= c0, sum[i][3] *= c1;
+            }
           }
         }
 #pragma unroll
@@ -691,6 +708,12 @@ attn_decode_kernel(const DecodeArgs a) {
       g_s = g_s + 1 == C::kStages ? 0 : g_s + 1;
     }
 
+    if constexpr (R == kSplit) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) o[0][i][u] += sum[i][u];
+    }
     // ------------------ the four warps' parts of the unit, joined ------------------
     // Eight heads at a time.  A part goes to this CTA's slot of the workspace:
     // the second one if it starts the unit (then it is the CTA's last), else
