@@ -88,7 +88,7 @@ int64_t dtype_bytes(int dtype) {
 nvq_status check_rows(const void* p, int64_t rows, int64_t width, int64_t stride, int64_t bytes) {
   if (rows == 0) return NVQ_OK;
   if (!p) return NVQ_ERR_INVALID_ARG;
-  if (stride < width || stride > (int64_t{1} << 40)) return NVQ_ERR_BAD_SHAPE;
+  if (stride < width || stride >= (int64_t{1} << 38)) return NVQ_ERR_BAD_SHAPE;   // below a tensor map's 2^40 bytes
   if (!aligned16(p) || stride * bytes % 16 != 0) return NVQ_ERR_MISALIGNED;
   return NVQ_OK;
 }
@@ -480,6 +480,7 @@ nvq_status nvq_attn_prefill(const void* q, int64_t q_stride, const void* k, int6
   nvq_status st = check_heads(n_heads, n_kv_heads, head_dim);
   if (st != NVQ_OK) return st;
   if (B > 65535 || total_q > kInt32Max / 2 || total_k > kInt32Max / 2) return NVQ_ERR_BAD_SHAPE;
+  if ((total_q / 128 + B) * n_heads > kInt32Max / 2) return NVQ_ERR_BAD_SHAPE;   // work items are counted in 32 bits
   if (B == 0 || total_q == 0) return NVQ_OK;
   if (!cu_q || !cu_k) return NVQ_ERR_INVALID_ARG;
   st = check_rows(q, total_q, n_heads * head_dim, q_stride, 2);

@@ -4,7 +4,9 @@
  * The library computes the fused dequantise-and-dot product used in
  * quantised LLM inference: 4-bit block-scaled weights (NVFP4) times 8-bit
  * block-quantised activations (Q8_0), for decode (matrix-vector, M = 1..16)
- * and prefill (GEMM, M up to thousands of tokens).
+ * and prefill (GEMM, M up to thousands of tokens); and the attention between
+ * those products: a paged key-value cache in Q8_0, the attention of new tokens
+ * over it, and the attention of packed prompts.
  *
  * Sources of the operations (web pages, cited by title and section):
  *  - "HANDOFF: flint CPU optimization (Q4_1 + NVFP4)", section 3 "Code map
@@ -433,8 +435,9 @@ typedef struct nvq_kv_cache {
  *
  * k, v  device rows [rows, n_kv_heads, head_dim] of `dtype` (NVQ_F32,
  *       NVQ_F16, NVQ_BF16), finite; k_stride and v_stride are the elements
- *       from one row to the next (>= n_kv_heads * head_dim, a multiple of 16
- *       bytes), so slices of a fused projection's output can be passed.
+ *       from one row to the next (>= n_kv_heads * head_dim, below 2^38, a
+ *       multiple of 16 bytes), so slices of a fused projection's output can be
+ *       passed.
  * Row r of sequence b becomes position seq_lens[b] - (cu_seqlens[b+1] - r):
  * the packed rows are the sequence's last positions.  Rows from
  * cu_seqlens[B] on are padding and are not written; nor is a row whose
@@ -443,10 +446,13 @@ typedef struct nvq_kv_cache {
  * nvq_quantize_act_q8_0 of the rows as fp32.  A page that is written must
  * belong to one sequence of the call (pages shared by a common prefix are
  * read, not written): two rows written to one place leave either's values.
+ * Nothing is done where B or rows is 0.  cu_seqlens, seq_lens and
+ * block_table need only the alignment of int32.
  * Errors: NVQ_ERR_INVALID_ARG (NULL, negative sizes, unknown dtype),
  * NVQ_ERR_BAD_SHAPE (head_dim, page_size, a stride below the row's length,
- * sizes over 2^31 - 1), NVQ_ERR_MISALIGNED, NVQ_ERR_UNSUPPORTED_DEVICE,
- * NVQ_ERR_CUDA.
+ * sizes over 2^31 - 1, more than 65535 heads, a cache of 2^31 or more rows
+ * n_pages * n_kv_heads * page_size), NVQ_ERR_MISALIGNED,
+ * NVQ_ERR_UNSUPPORTED_DEVICE, NVQ_ERR_CUDA.
  */
 nvq_status nvq_kv_write(const nvq_kv_cache* cache, const void* k, int64_t k_stride,
                         const void* v, int64_t v_stride, int dtype,
@@ -495,7 +501,8 @@ nvq_status nvq_kv_read(const nvq_kv_cache* cache, void* k, int64_t k_stride, voi
  *           workspace.  Results do not depend on timing.
  * Errors: as nvq_kv_write, NVQ_ERR_WORKSPACE, NVQ_ERR_INVALID_ARG for a
  * scale that is not finite and positive, NVQ_ERR_BAD_SHAPE when n_heads is no
- * multiple of n_kv_heads.
+ * multiple of n_kv_heads, B is over 65535, a table row holds 2^31 or more
+ * tokens, or all rows' 64-token tiles of every key-value head may pass 2^31.
  */
 nvq_status nvq_attn_decode(const nvq_kv_cache* cache, const void* q, int64_t q_stride,
                            int dtype, const int32_t* seq_lens, const int32_t* block_table,
@@ -526,7 +533,10 @@ size_t nvq_attn_decode_workspace_size(int64_t B, int64_t n_heads, int64_t n_kv_h
  * the probabilities are rounded to `dtype` for the product with the values.
  * A row range outside total_q or total_k raises NVQ_FLAG_BAD_INDEX; the
  * sequence counts as having no keys, its rows inside total_q give zeros.
- * Errors: as nvq_attn_decode; NVQ_ERR_INVALID_ARG for another dtype.
+ * No workspace.  Results do not depend on timing.
+ * Errors: as nvq_attn_decode; NVQ_ERR_INVALID_ARG for another dtype,
+ * NVQ_ERR_BAD_SHAPE when total_q or total_k is 2^30 or more, B over 65535, or
+ * (total_q / 128 + B) * n_heads 2^30 or more.
  */
 nvq_status nvq_attn_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                             const void* v, int64_t v_stride, int dtype, const int32_t* cu_q,

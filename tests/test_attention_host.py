@@ -66,6 +66,7 @@ BAD_DEC = [(dict(q=None), ARG), (dict(out=None), ARG), (dict(lens=None), ARG), (
            (dict(B=-1), ARG), (dict(cols=-1), ARG), (dict(dtype=7), ARG), (dict(heads=0), ARG), (dict(heads=-4), ARG),
            (dict(scale=0.0), ARG), (dict(scale=-1.0), ARG), (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG),
            (dict(heads=5), SHAPE), (dict(heads=1 << 17), SHAPE), (dict(B=1 << 17), SHAPE), (dict(cols=1 << 28), SHAPE),
+           (dict(B=1 << 15, cols=1 << 20), SHAPE), (dict(q_stride=1 << 38), SHAPE),
            (dict(q_stride=255), SHAPE), (dict(out_stride=0), SHAPE), (dict(q_stride=260), ALIGN), (dict(q=p(8)), ALIGN),
            (dict(out=p(4)), ALIGN), (dict(ws=p(8)), ALIGN), (dict(ws=None), WS), (dict(nbytes=0), WS)]
 
@@ -95,6 +96,7 @@ BAD_PRE = [(dict(q=None), ARG), (dict(k=None), ARG), (dict(v=None), ARG), (dict(
            (dict(heads=0), ARG), (dict(kv=0), ARG), (dict(scale=0.0), ARG), (dict(scale=float("nan")), ARG),
            (dict(heads=3), SHAPE), (dict(dim=256), SHAPE), (dict(dim=0), SHAPE), (dict(B=1 << 17), SHAPE), (dict(tq=1 << 31), SHAPE),
            (dict(tk=1 << 31), SHAPE), (dict(qs=255), SHAPE), (dict(ks=64), SHAPE), (dict(vs=64), SHAPE), (dict(os=128), SHAPE),
+           (dict(qs=1 << 39), SHAPE), (dict(tq=1 << 29, heads=1 << 14, kv=1, qs=1 << 20, os=1 << 20), SHAPE),
            (dict(qs=260), ALIGN), (dict(ks=132), ALIGN), (dict(vs=132), ALIGN), (dict(os=260), ALIGN), (dict(q=p(8)), ALIGN),
            (dict(k=p(2)), ALIGN), (dict(v=p(4)), ALIGN), (dict(out=p(8)), ALIGN)]
 

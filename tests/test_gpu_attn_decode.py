@@ -203,3 +203,51 @@ def test_decode_chain():
         tol = o.tolerance(o.sum_abs_terms(o.subblock_sums(po.ref_codes, q), po.ref_scales, po.ref_g, d))
         assert np.all(np.abs(y.cpu().numpy() - want) <= tol)
     assert capi.error_flags() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_sequences_of_few_tokens(dtype):
+    """More sequences than one search round and than blocks of the grid, most of them short or empty."""
+    rng = np.random.default_rng(1)
+    lens = np.where(rng.random(700) < 0.4, 0, rng.integers(1, 90, 700)).tolist()
+    lens[-1], lens[40] = 0, 900
+    c = Cache(lens, 1, 16, 64, seed=5)
+    q = queries(700, 3, 64, dtype, 2)
+    cnt = counters(700, 3)
+    out = capi.attn_decode(c.device(), q, c.dev_lens(), c.dev_table(), cnt)
+    compare(c, q, out, dtype)
+    assert not cnt.any() and capi.error_flags() == 0
+
+
+def test_two_streams_at_once_with_their_own_counters():
+    """Calls that overlap on two streams, each with counters and workspace of its own."""
+    cases = []
+    for i, lens in enumerate(([3000], [700, 50, 1200])):
+        c = Cache(lens, 4, 16, 128, seed=i)
+        q = queries(len(lens), 8, 128, torch.float16, i)
+        args = (c.device(), q, c.dev_lens(), c.dev_table())
+        cases.append((c, q, args, counters(len(lens), 8), torch.cuda.Stream()))
+    want = [capi.attn_decode(*args, counters(len(c.lens), 8)) for c, q, args, _, _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, q, args, cnt, stream) in enumerate(cases):
+            ws = torch.empty(capi.lib().nvq_attn_decode_workspace_size(len(c.lens), 8, 4, 128), dtype=torch.uint8, device="cuda")
+            out = torch.empty_like(q)
+            torch.cuda.current_stream().synchronize()
+            got[i].append((capi.attn_decode(*args, cnt, out=out, workspace=ws, stream=stream), ws))
+    torch.cuda.synchronize()
+    for i, (c, q, args, cnt, _) in enumerate(cases):
+        assert not cnt.any() and all(torch.equal(o, want[i]) for o, _ in got[i])
+    compare(cases[0][0], cases[0][1], want[0], torch.float16)
+
+
+def test_pages_shared_by_a_prefix():
+    """Two sequences whose tables begin with the same pages."""
+    c = Cache([70, 40], 2, 16, 64, seed=4, extra_cols=0)
+    table = c.table.copy()
+    table[1, :2] = table[0, :2]                 # 32 common tokens, then its own page
+    c.table = table
+    q = queries(2, 4, 64, torch.float32, 1)
+    out = capi.attn_decode(c.device(), q, c.dev_lens(), c.dev_table(), counters(2, 4))
+    compare(c, q, out, torch.float32)

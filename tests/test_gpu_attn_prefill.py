@@ -210,3 +210,60 @@ def test_prompt_chain():
         assert np.all(np.abs(out.cpu().numpy() - ref) <= tol)
         done = lens
     assert capi.error_flags() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_shifted_scores_of_every_size(dim):
+    """Scores around a constant far from zero (a shared component of the keys),
+    up to where their differences are all that is left, and a reference that
+    has to move at each step."""
+    n, dtype = 400, torch.float16
+    q, k, v = rows(n, 2, dim, dtype, 1), rows(n, 1, dim, dtype, 2), rows(n, 1, dim, dtype, 3)
+    for shift, scale in ((20.0, 0.05), (200.0, 0.2), (2000.0, 1.0)):
+        qq, kk = q.clone(), k.clone()
+        qq[..., 0], kk[..., 0] = shift, shift
+        out = capi.attn_prefill(qq, kk, v, cu_of([n]), scale=scale)
+        compare(qq, kk, v, [n], [n], out, dtype, True, scale, f"shift {shift}")
+    steps = torch.arange(n, device="cuda").div(64, rounding_mode="floor").view(-1, 1).to(dtype)
+    for sign in (1, -1):
+        qq, kk = q.clone() * 0.1, k.clone()
+        qq[..., 1], kk[..., 1] = 1.0, sign * 12.0 * steps
+        out = capi.attn_prefill(qq, kk, v, cu_of([n]), scale=1.0)
+        compare(qq, kk, v, [n], [n], out, dtype, True, 1.0, f"steps {sign}")
+
+
+def test_infinite_scores_make_their_rows_nan_and_no_other():
+    n = 200
+    q, k, v = rows(n, 2, 64, torch.float16, 1), rows(n, 1, 64, torch.float16, 2), rows(n, 1, 64, torch.float16, 3)
+    clean = capi.attn_prefill(q, k, v, cu_of([n]))
+    kk = k.clone()
+    kk[90, 0, 5] = float("inf")
+    out = capi.attn_prefill(q, kk, v, cu_of([n]))
+    torch.cuda.synchronize()
+    assert torch.equal(out[:64], clean[:64])                     # other steps of 64 keys and rows of warps
+    assert torch.isfinite(out[:90].float()).all()
+    pos = q[90:, :, 5] > 0                                       # +infinity: inf - inf
+    assert torch.isnan(out[90:].float()[pos]).all()
+    neg = q[90:, :, 5] < 0                                       # -infinity: a key like a hidden one
+    assert torch.isfinite(out[90:].float()[neg]).all()
+    args = [x.double().cpu().numpy() for x in (q, k, v)]
+    keep = np.delete(np.arange(n), 90)
+    for i in (120, 199):
+        for h in range(2):
+            if float(q[i, h, 5]) < 0:
+                js = keep[keep <= i]
+                ref, a, e = o.attend_fp64(args[0][i:i + 1, h:h + 1], args[1][js], args[2][js], 64 ** -0.5)
+                check(out[i:i + 1, h:h + 1], ref, bound(ref, a, e, len(js), np.abs(args[2]).max(), torch.float16, torch.float16))
+
+
+def test_two_streams_at_once():
+    cases = []
+    for i, n in enumerate(([500, 3], [130] * 9)):
+        N = sum(n)
+        cases.append((rows(N, 4, 128, torch.bfloat16, i), rows(N, 2, 128, torch.bfloat16, i + 5), rows(N, 2, 128, torch.bfloat16, i + 9),
+                      cu_of(n), torch.cuda.Stream()))
+    want = [capi.attn_prefill(*c[:4]) for c in cases]
+    torch.cuda.synchronize()
+    got = [(i, capi.attn_prefill(*c[:4], stream=c[4], out=torch.empty_like(c[0]))) for _ in range(20) for i, c in enumerate(cases)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i]) for i, x in got)

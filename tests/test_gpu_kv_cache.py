@@ -149,3 +149,36 @@ def test_many_sequences_and_another_stream():
         want = [np.concatenate([c.values(b)[w] for b in range(B)]) for w in range(2)]
         assert np.array_equal(k.cpu().numpy(), want[0].astype(np.float32))
         assert np.array_equal(v.cpu().numpy(), want[1].astype(np.float32))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+def test_codes_next_to_rounding_borders(dtype):
+    """Blocks whose quotients lie on or next to a half, tiny and huge blocks,
+    against the activation quantiser (whose quotients are divisions)."""
+    rng = np.random.default_rng(3)
+    n, heads, dim = 64, 4, 128
+    x = np.empty((n, heads, dim // 32, 32), np.float32)
+    amax = np.float32(10.0) ** rng.uniform(-4, 4, (n, heads, dim // 32)).astype(np.float32)
+    if dtype == torch.float32:
+        amax.reshape(-1)[:6] = [1e-45, 3e-44, 1e-38, 1e-30, 8e6, 1e-37]
+    else:
+        amax = np.clip(amax, 1e-4, 6e4)
+        amax.reshape(-1)[:3] = [6e-8, 2e-6, 65504]
+    d32 = amax / np.float32(127)
+    half = rng.integers(-127, 127, x.shape).astype(np.float32) + np.float32(0.5)
+    x[:] = half * d32[..., None]
+    nudge = rng.integers(-2, 3, x.shape)
+    for _ in range(2):
+        x = np.where(nudge > 0, np.nextafter(x, np.float32(np.inf)), np.where(nudge < 0, np.nextafter(x, np.float32(-np.inf)), x))
+        nudge = np.sign(nudge) * (np.abs(nudge) - 1)
+    x[..., 0] = amax
+    t = torch.from_numpy(x.reshape(n, heads, dim)).to(dtype).cuda()
+    c = capi.kv_cache(4, heads, 16, dim)
+    table = torch.tensor([[3, 1, 0, 2]], dtype=torch.int32).cuda()
+    capi.kv_write(c, t, t, cu_of([n]), torch.tensor([n], dtype=torch.int32).cuda(), table)
+    q, d = capi.quantize_act_q8_0(t.float().reshape(n * heads, dim))
+    pos = torch.arange(n, device="cuda")
+    pg = table[0].long()[pos // 16]
+    for codes, scales in (c[:2], c[2:]):
+        assert torch.equal(codes[pg, :, pos % 16].reshape(-1, dim), q)
+        assert torch.equal(scales[pg, :, pos % 16].reshape(-1, dim // 32), d)
