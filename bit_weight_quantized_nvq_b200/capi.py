@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from contextlib import nullcontext
+from functools import lru_cache
 
 import numpy as np
 import torch
@@ -343,7 +343,6 @@ def debug_subblock_sums(codes: torch.Tensor, scales: torch.Tensor, g: float, q: 
 #: NVQ_F32, NVQ_F16, NVQ_BF16
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _I8, _I32, _F16 = torch.int8, torch.int32, torch.float16
-_HERE = nullcontext()
 
 # The checks below run before every launch of a decode step, so they compare
 # device numbers (-1: not a CUDA device) and whole shapes.
@@ -449,17 +448,30 @@ def kv_read(cache, cu_seqlens: torch.Tensor, seq_lens: torch.Tensor, block_table
     dev = cache[0].get_device()
     c = _cache(cache, dev)
     shape = (rows, c.n_kv_heads, c.head_dim)
+    ks = vs = c.n_kv_heads * c.head_dim
     if k is None:
         k = cache[0].new_empty(shape, dtype=dtype)
+    else:
+        ks = _rows("k", k, shape, k, dev)
     if v is None:
         v = k.new_empty(shape)
+    else:
+        vs = _rows("v", v, shape, k, dev)
     dt = _dtype(k)
-    ks, vs = _rows("k", k, shape, k, dev), _rows("v", v, shape, k, dev)
     B, cols = seq_lens.shape[0], block_table.shape[-1]
     _launch(dev, stream, "nvq_kv_read", _lib.nvq_kv_read, c, k.data_ptr(), ks, v.data_ptr(), vs, dt,
             _index("cu_seqlens", cu_seqlens, dev, (B + 1,)), _index("seq_lens", seq_lens, dev, (B,)),
             _index("block_table", block_table, dev, (B, cols)), B, cols, rows)
     return k, v
+
+
+@lru_cache(maxsize=None)
+def _decode_workspace(dev: int, B: int, H: int, Hk: int, D: int) -> int:
+    """Workspace bytes of nvq_attn_decode on a device (a function of sizes)."""
+    if dev < 0:
+        raise ValueError("nvq_attn_decode: tensors on a CUDA device expected")
+    with torch.cuda.device(dev):
+        return max(16, int(_lib.nvq_attn_decode_workspace_size(B, H, Hk, D)))
 
 
 def attn_decode(cache, q: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
@@ -486,11 +498,7 @@ def attn_decode(cache, q: torch.Tensor, seq_lens: torch.Tensor, block_table: tor
     else:
         os_ = _rows("out", out, shape, q, dev)
     if workspace is None:
-        if dev < 0:
-            raise ValueError("nvq_attn_decode: tensors on a CUDA device expected")
-        with torch.cuda.device(dev) if dev != torch._C._cuda_getDevice() else _HERE:
-            nbytes = _lib.nvq_attn_decode_workspace_size(B, H, c.n_kv_heads, D)
-        workspace = q.new_empty(max(nbytes, 16), dtype=torch.uint8)
+        workspace = q.new_empty(_decode_workspace(dev, B, H, c.n_kv_heads, D), dtype=torch.uint8)
     _launch(dev, stream, "nvq_attn_decode", _lib.nvq_attn_decode, c, q.data_ptr(), qs, dt,
             _index("seq_lens", seq_lens, dev, (B,)), _index("block_table", block_table, dev, (B, cols)),
             B, cols, H, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,

@@ -99,6 +99,7 @@ struct Item {
   int steps[2];              // steps of 64 keys of each (0: it sees none)
   bool on[2];                // whether the tile has queries
   int clean_from;            // the first key that some query does not see
+  int scan = 0, before = 0;  // where the search for the next one starts: sequence, tiles before it
   __device__ int blocks() const { return (max(steps[0], steps[1]) + 1) / 2; }   // K and V blocks loaded
   // keys that query i (of the sequence) sees
   __device__ int limit(int i, int causal) const { return causal ? min(m, i + m - n + 1) : m; }
@@ -129,8 +130,8 @@ __device__ __forceinline__ int item_of(int t) {
 // no such item.
 __device__ __forceinline__ bool find_item(const Args& a, int x, int lane, Item& it) {
   const int rows = a.two_heads ? kTile : 2 * kTile;
-  int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
+  // a CTA's items come in order, so the search goes on where it was
+  for (int& b0 = it.scan; b0 < a.B; b0 += 32) {
     int q0 = 0, n = 0, k0 = 0, m = 0;
     if (b0 + lane < a.B) sequence(a, b0 + lane, q0, n, k0, m);
     const int tiles = (n + rows - 1) / rows;
@@ -140,7 +141,7 @@ __device__ __forceinline__ bool find_item(const Args& a, int x, int lane, Item& 
       const int u = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += u;
     }
-    const int at = x / a.pairs - before;
+    const int at = x / a.pairs - it.before;
     const unsigned hit = __ballot_sync(0xffffffffu, incl > at);
     if (hit != 0) {
       const int src = __ffs(hit) - 1;
@@ -163,7 +164,7 @@ __device__ __forceinline__ bool find_item(const Args& a, int x, int lane, Item& 
       }
       return true;
     }
-    before += __shfl_sync(0xffffffffu, incl, 31);
+    it.before += __shfl_sync(0xffffffffu, incl, 31);
   }
   return false;
 }
