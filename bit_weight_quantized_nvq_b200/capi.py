@@ -396,6 +396,17 @@ def _cache(cache, dev: int) -> KVCache:
     return KVCache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), n, h, p, d)
 
 
+def _empty(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tensor:
+    """A new tensor for a call on `stream`: allocated there, so that memory
+    freed behind the call is not handed to another stream before it ran."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _launch(dev: int, stream, name: str, fn, *args) -> None:
     """Call an entry point with device `dev` current, on its current stream
     unless another is given."""
@@ -450,11 +461,11 @@ def kv_read(cache, cu_seqlens: torch.Tensor, seq_lens: torch.Tensor, block_table
     shape = (rows, c.n_kv_heads, c.head_dim)
     ks = vs = c.n_kv_heads * c.head_dim
     if k is None:
-        k = cache[0].new_empty(shape, dtype=dtype)
+        k = _empty(cache[0], shape, dtype, stream)
     else:
         ks = _rows("k", k, shape, k, dev)
     if v is None:
-        v = k.new_empty(shape)
+        v = _empty(k, shape, k.dtype, stream)
     else:
         vs = _rows("v", v, shape, k, dev)
     dt = _dtype(k)
@@ -493,12 +504,12 @@ def attn_decode(cache, q: torch.Tensor, seq_lens: torch.Tensor, block_table: tor
             or counters.numel() < B * H:
         raise ValueError(f"counters: contiguous int32 [{B * H}] on device {dev} expected")
     if out is None:
-        out = q.new_empty(shape)
+        out = _empty(q, shape, q.dtype, stream)
         os_ = H * D
     else:
         os_ = _rows("out", out, shape, q, dev)
     if workspace is None:
-        workspace = q.new_empty(_decode_workspace(dev, B, H, c.n_kv_heads, D), dtype=torch.uint8)
+        workspace = _empty(q, _decode_workspace(dev, B, H, c.n_kv_heads, D), torch.uint8, stream)
     _launch(dev, stream, "nvq_attn_decode", _lib.nvq_attn_decode, c, q.data_ptr(), qs, dt,
             _index("seq_lens", seq_lens, dev, (B,)), _index("block_table", block_table, dev, (B, cols)),
             B, cols, H, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
@@ -525,7 +536,7 @@ def attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.
     ks, vs = _rows("k", k, (keys, Hk, D), q, dev), _rows("v", v, (keys, Hk, D), q, dev)
     B = cu_q.shape[0] - 1
     if out is None:
-        out = q.new_empty(shape)
+        out = _empty(q, shape, q.dtype, stream)
         os_ = H * D
     else:
         os_ = _rows("out", out, shape, q, dev)

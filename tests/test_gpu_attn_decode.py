@@ -251,3 +251,21 @@ def test_pages_shared_by_a_prefix():
     q = queries(2, 4, 64, torch.float32, 1)
     out = capi.attn_decode(c.device(), q, c.dev_lens(), c.dev_table(), counters(2, 4))
     compare(c, q, out, torch.float32)
+
+
+def test_memory_of_a_call_on_another_stream_is_not_reused_under_it():
+    """The binding's own workspace and output belong to the call's stream."""
+    c = Cache([9000], 4, 64, 128, seed=3)
+    q = queries(1, 8, 128, torch.float32, 3)
+    dev, lens, table, cnt = c.device(), c.dev_lens(), c.dev_table(), counters(1, 8)
+    want = capi.attn_decode(dev, q, lens, table, cnt)
+    nbytes = capi.lib().nvq_attn_decode_workspace_size(1, 8, 4, 128)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(30):
+        got.append(capi.attn_decode(dev, q, lens, table, cnt, stream=side))
+        torch.full((nbytes // 4,), float("nan"), device="cuda")
+    got.append(capi.attn_decode(dev, q, lens, table, cnt, stream=side.cuda_stream))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in got) and not cnt.any()
