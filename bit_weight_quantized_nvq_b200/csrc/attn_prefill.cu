@@ -22,6 +22,7 @@
 //               about as long for a small MMA as the tensor core for one of
 //               N = 128, so each tile has its own
 //   warp 10     TMA: both Q tiles, then K and V blocks of 128 keys into a ring
+//   warp 11     cleans V blocks that some query does not see all of (below)
 //
 // The two tiles share K and V: two heads of one key-value head with the same
 // 128 queries where the group is even, else 256 queries of one head.  Work
@@ -35,11 +36,11 @@
 // product before, rescales O and forms the step again.
 //
 // A key behind a query's last one gets p = 0, but 0 * NaN is not 0: before a
-// block with such keys is used, the softmax warps zero the rows of V behind
-// the sequence's end in shared memory, and replace NaN and infinities in rows
-// that only some of the queries see by 0 and add them to those queries'
-// results at the end.  Both tiles' warps do all of it (the second finds it
-// done), as either may be the first to release its product.
+// block with such keys is used, its rows of V behind the sequence's end are
+// zeroed in shared memory, and NaN and infinities in rows that only some of
+// the queries see are replaced by 0 and added to those queries' results at
+// the end.  A warp of its own does it ahead of the products; done by the
+// softmax warps it doubled the time of their last steps.
 #include <algorithm>
 #include <climits>
 #include <mutex>
@@ -59,8 +60,9 @@ namespace {
 
 constexpr int kTile = 128;           // queries of a tile, keys of a block
 constexpr int kStep = 64;            // keys of a step: half a block
-constexpr int kThreads = 352;
-constexpr int kMmaWarp = 8, kLoadWarp = 10;
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kCleanWarp = 11;
+constexpr int kRaw = 4;              // V blocks on their way to be cleaned (the ring holds no more)
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr float kLazy = 256.0f;       // how far a step's exponentials may add up before the reference moves
 constexpr float kLarge = 1024.0f;     // exponents from here on are formed as differences first
@@ -76,7 +78,7 @@ struct Cfg {
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kOffRing = 2 * kBlock;
   static constexpr int kOffBars = kOffRing + kStages * kBlock;
-  static constexpr int kBars = 2 * kStages + 2 + 4 + 4 + 2 + 2 + 1;
+  static constexpr int kBars = 2 * kStages + 2 + 4 + 4 + 2 + 2 + 1 + kRaw;
   static constexpr int kOffMisc = kOffBars + 8 * kBars;
   static constexpr int kSmem = kOffMisc + 16 + 4 * kItemFlags + 1024;
 };
@@ -258,44 +260,49 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return dev::h2_bits(__floats2half2_rn(lo, hi));
 }
 
-// 128 threads (thread r of them): rows `from`.. of a step of V in shared memory:
-// those from `end` on are set to zero, in the others NaN and infinities.
-// *found is set before one is taken out, so whoever finds it gone finds the flag
-// set too.  Eight lanes take a row of 128 bytes; the swizzle only permutes it.
-// Nothing is written where nothing changes, since the other tile's product
-// may be reading a block that is clean.
+// One warp: rows `from`.. of a V block in shared memory; those from `end` on are
+// set to zero, in the others NaN and infinities.  Returns whether this lane
+// met one.  Eight lanes take a row of 128 bytes; the swizzle only permutes it.
 template <int SUBS, bool BF16>
-__device__ __noinline__ void clean_values(unsigned char* block, int sub_bytes, int from, int end, int r,
-                                          volatile int* found) {
+__device__ __noinline__ bool clean_values(unsigned char* block, int sub_bytes, int from, int end, int lane) {
   constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
-  for (int row = from + (r >> 3); row < kStep; row += 16) {
+  bool any = false;
+  // whole rows of zeros first, then the check, several loads in flight
+  for (int row = max(from, end) + (lane >> 3); row < kTile; row += 4)
 #pragma unroll
-    for (int i = 0; i < SUBS; ++i) {
-      uint4* p = reinterpret_cast<uint4*>(block + i * sub_bytes + row * 128) + (r & 7);
-      uint4 w = *p;
-      if (row >= end) {
-        if ((w.x | w.y | w.z | w.w) != 0) *p = make_uint4(0, 0, 0, 0);
-        continue;
+    for (int i = 0; i < SUBS; ++i)
+      reinterpret_cast<uint4*>(block + i * sub_bytes + row * 128)[lane & 7] = make_uint4(0, 0, 0, 0);
+  constexpr int kBatch = 4;
+  for (int row0 = from + (lane >> 3); row0 < min(end, kTile); row0 += 4 * kBatch) {
+    uint4 w[kBatch][SUBS];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int i = 0; i < SUBS; ++i) {
+        const int row = row0 + 4 * k;
+        w[k][i] = row < min(end, kTile) ? reinterpret_cast<const uint4*>(block + i * sub_bytes + row * 128)[lane & 7]
+                                        : make_uint4(0, 0, 0, 0);
       }
-      uint32_t* u = &w.x;
-      bool bad = false;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t hit = ((u[e] & kExp) + kOne) & 0x80008000u;   // exponent all ones
-        if (hit != 0) {
-          bad = true;
-          if (hit & 0x8000u) u[e] &= 0xFFFF0000u;
-          if (hit & 0x80000000u) u[e] &= 0x0000FFFFu;
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int i = 0; i < SUBS; ++i) {
+        uint32_t u[4] = {w[k][i].x, w[k][i].y, w[k][i].z, w[k][i].w}, hits = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) hits |= ((u[e] & kExp) + kOne) & 0x80008000u;     // exponent all ones
+        if (hits != 0) {
+          any = true;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t hit = ((u[e] & kExp) + kOne) & 0x80008000u;
+            if (hit & 0x8000u) u[e] &= 0xFFFF0000u;
+            if (hit & 0x80000000u) u[e] &= 0x0000FFFFu;
+          }
+          reinterpret_cast<uint4*>(block + i * sub_bytes + (row0 + 4 * k) * 128)[lane & 7] = make_uint4(u[0], u[1], u[2], u[3]);
         }
       }
-      if (bad) {
-        *found = 1;
-        __threadfence_block();
-        *p = w;
-      }
-    }
   }
-  __threadfence_block();
+  return any;
 }
 
 template <int D, bool BF16>
@@ -316,6 +323,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   auto o_done = [&](int s) { return bar(2 * C::kStages + 10 + s); };
   auto o_full = [&](int s) { return bar(2 * C::kStages + 12 + s); };
   const uint32_t mma_done = bar(2 * C::kStages + 14);
+  auto v_raw = [&](int i) { return bar(2 * C::kStages + 15 + i % kRaw); };
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* found = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);
@@ -337,6 +345,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       ptx::mbar_init(o_full(s), 1);
     }
     ptx::mbar_init(mma_done, 2);
+    for (int i = 0; i < kRaw; ++i) ptx::mbar_init(v_raw(i), 1);
     *abort_flag = 0;
     for (int i = 0; i < kItemFlags; ++i) found[i] = 0;
     ptx::fence_mbar_init();
@@ -372,18 +381,23 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   if (warp == kLoadWarp) {
     // --------------------------------- copies ---------------------------------
     int g = 0;                 // K and V blocks issued
+    int raws = 0;              // V blocks to be cleaned
     bool ok = true;
     Item it;
-    auto block = [&](const CUtensorMap* map, int col, int row) {
+    // a V block to be cleaned is announced to the warp that does it, which
+    // announces it as full
+    auto block = [&](const CUtensorMap* map, int col, int row, bool clean) {
       const int s = g % C::kStages;
       if (!warp_wait(kv_empty(s), ((g / C::kStages) & 1) ^ 1)) return false;
       if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(kv_full(s), C::kBlock);
+        const uint32_t b = clean ? v_raw(raws) : kv_full(s);
+        ptx::mbar_arrive_expect_tx(b, C::kBlock);
         for (int i = 0; i < C::kSubs; ++i)
-          ptx::tma_load_2d(base + C::kOffRing + s * C::kBlock + i * C::kSub, map, col + 64 * i, row, kv_full(s));
+          ptx::tma_load_2d(base + C::kOffRing + s * C::kBlock + i * C::kSub, map, col + 64 * i, row, b);
       }
       __syncwarp();
       ++g;
+      raws += clean;
       return true;
     };
     int items = 0;
@@ -403,13 +417,40 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       ++items;
       const int col = it.head[0] / a.group * D;
       for (int j = 0; ok && j < it.blocks(); ++j)
-        ok = block(&k_map, col, it.k0 + j * kTile) && block(&v_map, col, it.k0 + j * kTile);
+        ok = block(&k_map, col, it.k0 + j * kTile, false) &&
+             block(&v_map, col, it.k0 + j * kTile, (j + 1) * kTile > it.clean_from);
     }
     if (*abort_flag) {
       // the MMAs may have stopped: wait for the copies in flight
       if (items > 0) ptx::mbar_wait_bounded(q_full, (items - 1) & 1, nullptr, kWaitLimitNs);
+      for (int i = max(0, raws - kRaw); i < raws; ++i)
+        ptx::mbar_wait_bounded(v_raw(i), (i / kRaw) & 1, nullptr, kWaitLimitNs);
       for (int i = max(0, g - C::kStages); i < g; ++i)
         ptx::mbar_wait_bounded(kv_full(i % C::kStages), (i / C::kStages) & 1, nullptr, kWaitLimitNs);
+    }
+  } else if (warp == kCleanWarp) {
+    // ------------------------ V blocks with unseen keys ------------------------
+    int g = 0, items = 0, raws = 0;
+    bool ok = true;
+    Item it;
+    for (int t = 0, x; ok && (x = item_of(t), t * static_cast<int>(gridDim.x) < a.max_items); ++t) {
+      if (!find_item(a, x, lane, it) || it.blocks() == 0) continue;
+      for (int j = max(0, it.clean_from / kTile); ok && j < it.blocks(); ++j) {
+        const int v = g + 2 * j + 1;
+        ok = warp_wait(v_raw(raws), (raws / kRaw) & 1);
+        ++raws;
+        if (!ok) break;
+        const bool met = clean_values<C::kSubs, BF16>(smem + C::kOffRing + (v % C::kStages) * C::kBlock, C::kSub,
+                                                      max(0, it.clean_from - j * kTile), it.m - j * kTile, lane);
+        // the item's own number, so that nothing has to be reset; the ring
+        // keeps this warp fewer items ahead than there are places
+        if (met) found[items % kItemFlags] = items + 1;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(kv_full(v % C::kStages));
+      }
+      g += 2 * it.blocks();
+      ++items;
     }
   } else if (warp >= kMmaWarp) {
     // ------------------------------ MMAs of tile s ------------------------------
@@ -430,8 +471,6 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       const int N = it.blocks(), steps = s ? it.steps[1] : it.steps[0];
       ok = warp_wait(q_full, items & 1);
       if (!ok) break;
-      // the flag of an item to come; the ring keeps the tiles fewer items apart
-      if (s == 0 && lane == 0) found[(items + kItemFlags / 2) % kItemFlags] = 0;
       auto scores = [&](int i) {       // S of step i
         const int k = g + (i & ~1);
         if (!(i & 1) && !wait_block(k)) return false;
@@ -491,7 +530,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + 128 * s, t_o = tmem + lanes + 256 + 128 * s;
     const float c = a.scale_log2;
-    int g = 0, items = 0;
+    int items = 0;
     uint32_t s_par = 0;                            // parity of each buffer's next S
     int sent = 0, o_count = 0;                     // steps handed on, results taken, over all items
     bool ok = true;
@@ -499,9 +538,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
     for (int t = 0, x; ok && (x = item_of(t), t * static_cast<int>(gridDim.x) < a.max_items); ++t) {
       if (!find_item(a, x, lane, it)) continue;
       const int item = items;
-      const int g0 = g;                            // ring place of K_0
       if (it.blocks() > 0) ++items;
-      g += 2 * it.blocks();
       // this tile's values (selected, so that they stay in registers)
       if (!(s ? it.on[1] : it.on[0])) continue;
       const int row = (s ? it.row[1] : it.row[0]) + r;       // query of the sequence
@@ -593,17 +630,6 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         }
         if (!ok) break;
         l += sum;
-        if ((i + 1) * kStep > it.clean_from) {
-          // V has keys here that some query does not see (its place in the ring
-          // is this one until P is released)
-          const int vb = g0 + (i | 1);
-          ok = warp_wait(kv_full(vb % C::kStages), (vb / C::kStages) & 1);
-          if (!ok) break;
-          clean_values<C::kSubs, BF16>(smem + C::kOffRing + (vb % C::kStages) * C::kBlock + b * kStep * 128, C::kSub,
-                                       max(0, it.clean_from - i * kStep), it.m - i * kStep, r,
-                                       found + item % kItemFlags);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
@@ -619,7 +645,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         ptx::tc_fence_after();
       }
       const float inv = l > 0.0f ? __fdividef(1.0f, l) : l;       // nothing seen: 0; NaN stays
-      const bool patch = some && found[item % kItemFlags] != 0;
+      const bool patch = some && found[item % kItemFlags] == item + 1;
       using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
       T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(it.q0) + row) * a.out_stride + head * D;
 #pragma unroll
