@@ -251,6 +251,12 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// 32 bytes, a whole sector, from one lane.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if (BF16) {
@@ -530,6 +536,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + 128 * s, t_o = tmem + lanes + 256 + 128 * s;
     const float c = a.scale_log2;
+    const bool sectors = ((reinterpret_cast<uintptr_t>(a.out) | (2 * a.out_stride)) & 31) == 0;
     int items = 0;
     uint32_t s_par = 0;                            // parity of each buffer's next S
     int sent = 0, o_count = 0;                     // steps handed on, results taken, over all items
@@ -557,10 +564,17 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         ptx::tmem_ld_32cols(t_s + kStep * b + 32, v[1]);
         wait_ld_32(v[0]);
         wait_ld_32(v[1]);
-        if (__any_sync(0xffffffffu, seen < kStep)) {
+        // rows see more keys the later they are: lane 0 the fewest, and only
+        // the columns that it does not see are looked at
+        const int least = __shfl_sync(0xffffffffu, seen, 0);
+        if (least < kStep) {
 #pragma unroll
-          for (int e = 0; e < kStep; ++e)
-            if (e >= seen) v[e / 32][e % 32] = 0xFF800000u;       // -infinity
+          for (int q = 0; q < kStep; q += 8)
+            if (least < q + 8) {
+#pragma unroll
+              for (int e = q; e < q + 8; ++e)
+                if (e >= seen) v[e / 32][e % 32] = 0xFF800000u;       // -infinity
+            }
         }
         // the step's maximum (NaN if a score is); it is not needed as a rule
         auto largest = [&]() -> float {
@@ -671,11 +685,23 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           }
         }
         if (row < it.n) {
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(out + 32 * q + i) =
-                make_uint4(pack2<BF16>(e[i], e[i + 1]), pack2<BF16>(e[i + 2], e[i + 3]),
-                           pack2<BF16>(e[i + 4], e[i + 5]), pack2<BF16>(e[i + 6], e[i + 7]));
+          for (int i = 0; i < 16; ++i) w[i] = pack2<BF16>(e[2 * i], e[2 * i + 1]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // a lane's row is its own, so every store goes to 32 places: whole
+            // sectors where the rows allow it
+            if (sectors) {
+              const uint32_t x8[8] = {w[8 * h], w[8 * h + 1], w[8 * h + 2], w[8 * h + 3],
+                                      w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7]};
+              store32(out + 32 * q + 16 * h, x8);
+            } else {
+              uint4* to = reinterpret_cast<uint4*>(out + 32 * q + 16 * h);
+              to[0] = make_uint4(w[8 * h], w[8 * h + 1], w[8 * h + 2], w[8 * h + 3]);
+              to[1] = make_uint4(w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7]);
+            }
+          }
         }
       }
     }
