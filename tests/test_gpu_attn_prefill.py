@@ -267,3 +267,25 @@ def test_two_streams_at_once():
     got = [(i, capi.attn_prefill(*c[:4], stream=c[4], out=torch.empty_like(c[0]))) for _ in range(20) for i, c in enumerate(cases)]
     torch.cuda.synchronize()
     assert all(torch.equal(x, want[i]) for i, x in got)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_rows_apart_by_an_odd_number_of_16_bytes(dim):
+    """Rows of every operand 16 bytes further apart than their heads fill, so no
+    row but the first lies on a 32-byte boundary; nothing between them changes."""
+    n, H, kv = [70, 133], 4, 2
+    N = sum(n)
+
+    def spread(x):
+        rows_, h, d = x.shape
+        buf = torch.full((rows_, h * d + 8), 5.0, dtype=x.dtype, device="cuda")
+        view = buf[:, :h * d].unflatten(1, (h, d))
+        view.copy_(x)
+        return buf, view
+
+    q, k, v = (spread(rows(N, h, dim, torch.bfloat16, i)) for i, h in enumerate((H, kv, kv)))
+    buf, out = spread(torch.zeros(N, H, dim, dtype=torch.bfloat16, device="cuda"))
+    capi.attn_prefill(q[1], k[1], v[1], cu_of(n), out=out)
+    compare(q[1], k[1], v[1], n, n, out, torch.bfloat16, True)
+    assert (buf[:, H * dim:] == 5).all()
+    assert torch.equal(out, capi.attn_prefill(q[1].contiguous(), k[1].contiguous(), v[1].contiguous(), cu_of(n)))
