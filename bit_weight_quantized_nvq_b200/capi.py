@@ -400,6 +400,8 @@ def _empty(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tenso
     """A new tensor for a call on `stream`: allocated there, so that memory
     freed behind the call is not handed to another stream before it ran."""
     if stream is None:
+        if shape == like.shape and dtype is like.dtype and like.is_contiguous():
+            return torch.empty_like(like)
         return like.new_empty(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
