@@ -22,7 +22,8 @@
 // of 16 alike.  The chunks are swizzled so that both read patterns below are
 // free of bank conflicts.  (One warp issuing TMA boxes for all four was the
 // first form: with pages of 16 tokens, 16 small copies a tile, the copies alone
-// took 66 us for 162 MB; with pages of 128, 127 us for 706 MB.)
+// took 66 us for 162 MB; with pages of 128, 127 us for 706 MB.
+// Each warp issuing TMA boxes of its own: 174 us for the 706 MB, against 156.)
 //
 // Scores (m16n8k16, fp16 operands): A holds the queries, B the codes of 8
 // tokens, which are exact in
@@ -41,6 +42,11 @@
 // These are warp-level MMAs: there are at most 16 query rows per key-value
 // head, an eighth of the smallest tcgen05 tile, and the operands change
 // with every tile, so the tensor pipe is not what bounds this kernel.
+//
+// Measured, cold L2: 64 sequences of 2048..8192 tokens, 64 over 8 heads of 128,
+// fp16, 156 us (4.5 TB/s); one of 131072, fp32, 84 us (3.4); 24 of 1..6000 with
+// pages of 16, bf16, 53 us (3.0).  Copies alone take 125 us of the 156; the
+// issue slots are 59 % full.
 #include <algorithm>
 
 #include <cuda_fp16.h>

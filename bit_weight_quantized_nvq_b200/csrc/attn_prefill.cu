@@ -40,7 +40,11 @@
 // zeroed in shared memory, and NaN and infinities in rows that only some of
 // the queries see are replaced by 0 and added to those queries' results at
 // the end.  A warp of its own does it ahead of the products; done by the
-// softmax warps it doubled the time of their last steps.
+// softmax warps, 2048 tokens of 40 heads took 80 us instead of 71.
+//
+// Measured, cold L2: 8192 tokens, 40 over 8 heads of 128, bf16, causal, 625 us
+// (1100 TFLOP/s; 711 us back to back, at the power limit); 2048 tokens, 40
+// heads, fp16, 67 us.
 #include <algorithm>
 #include <climits>
 #include <mutex>
