@@ -336,6 +336,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   auto v_raw = [&](int i) { return bar(2 * C::kStages + 15 + i % kRaw); };
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  volatile int* issued = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
   volatile int* found = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -357,6 +358,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
     ptx::mbar_init(mma_done, 2);
     for (int i = 0; i < kRaw; ++i) ptx::mbar_init(v_raw(i), 1);
     *abort_flag = 0;
+    *issued = 0;
     for (int i = 0; i < kItemFlags; ++i) found[i] = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tensormap(&q_map);
@@ -378,11 +380,20 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
     *abort_flag = 1;
     atomicOr(&g_attn_prefill_error_flags, 1u);
   };
-  // The whole warp waits, one lane acts (see the prefill GEMM).
+  // The whole warp waits, one lane acts (see the prefill GEMM).  The limit holds
+  // from the last block that was loaded on: a warp may wait through any number
+  // of items that need nothing of it (the cleaner through those without unseen
+  // keys, a tile's softmax through those with one tile).  The blocks are
+  // counted, so the waits still end.
   auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(b, parity))) return true;
-    const bool got = ptx::mbar_wait_bounded(b, parity, abort_flag, kWaitLimitNs);
-    if (__all_sync(0xffffffffu, got)) return true;
+    for (int before = __shfl_sync(0xffffffffu, *issued, 0);;) {
+      const bool got = ptx::mbar_wait_bounded(b, parity, abort_flag, kWaitLimitNs);
+      if (__all_sync(0xffffffffu, got)) return true;
+      const int now = __shfl_sync(0xffffffffu, *issued, 0);
+      if (now == before || __any_sync(0xffffffffu, *abort_flag != 0)) break;
+      before = now;
+    }
     fail();
     return false;
   };
@@ -404,6 +415,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         ptx::mbar_arrive_expect_tx(b, C::kBlock);
         for (int i = 0; i < C::kSubs; ++i)
           ptx::tma_load_2d(base + C::kOffRing + s * C::kBlock + i * C::kSub, map, col + 64 * i, row, b);
+        *issued = g + 1;
       }
       __syncwarp();
       ++g;

@@ -289,3 +289,27 @@ def test_rows_apart_by_an_odd_number_of_16_bytes(dim):
     compare(q[1], k[1], v[1], n, n, out, torch.bfloat16, True)
     assert (buf[:, H * dim:] == 5).all()
     assert torch.equal(out, capi.attn_prefill(q[1].contiguous(), k[1].contiguous(), v[1].contiguous(), cu_of(n)))
+
+
+def test_a_long_call_with_unseen_keys_only_at_its_end():
+    """A call of more than the 4 s that a wait may last without progress: the
+    first sequence's keys are all seen (not causal, whole blocks), so whatever
+    takes care of unseen ones has nothing to do until the second."""
+    n, m = [1310720, 1], [1 << 24, 100]
+    k = torch.zeros(sum(m), 1, 64, dtype=torch.bfloat16, device="cuda")
+    v = torch.ones(sum(m), 1, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.ones(sum(n), 1, 64, dtype=torch.bfloat16, device="cuda")
+    for t, seed in ((q, 1), (k, 2), (v, 3)):
+        i = n[0] if t is q else m[0]
+        t[i:] = rows(len(t) - i, 1, 64, torch.bfloat16, seed)
+    capi.error_flags(clear=True)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    out = capi.attn_prefill(q, k, v, cu_of(n), cu_of(m), causal=False)
+    end.record()
+    torch.cuda.synchronize()
+    print(f"{start.elapsed_time(end):.0f} ms")
+    assert capi.error_flags() == 0
+    # equal scores and values: the sums are whole numbers up to 2^24, exact
+    assert (out[:n[0]] == 1).all()
+    compare(q[n[0]:], k[m[0]:], v[m[0]:], n[1:], m[1:], out[n[0]:], torch.bfloat16, False)
