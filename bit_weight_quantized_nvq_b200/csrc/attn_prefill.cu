@@ -70,7 +70,6 @@ constexpr int kRaw = 4;              // V blocks on their way to be cleaned (the
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr float kLazy = 256.0f;       // how far a step's exponentials may add up before the reference moves
 constexpr float kLarge = 1024.0f;     // exponents from here on are formed as differences first
-constexpr int kItemFlags = 16;       // found flags of the last items
 
 __device__ unsigned int g_attn_prefill_error_flags = 0;   // bit 0: a wait timed out, bit 1: a bad index
 
@@ -84,7 +83,7 @@ struct Cfg {
   static constexpr int kOffBars = kOffRing + kStages * kBlock;
   static constexpr int kBars = 2 * kStages + 2 + 4 + 4 + 2 + 2 + 1 + kRaw;
   static constexpr int kOffMisc = kOffBars + 8 * kBars;
-  static constexpr int kSmem = kOffMisc + 16 + 4 * kItemFlags + 1024;
+  static constexpr int kSmem = kOffMisc + 16 + 1024;
 };
 
 struct Args {
@@ -337,7 +336,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* issued = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
-  volatile int* found = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);
+  volatile int* found = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 12);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -359,7 +358,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
     for (int i = 0; i < kRaw; ++i) ptx::mbar_init(v_raw(i), 1);
     *abort_flag = 0;
     *issued = 0;
-    for (int i = 0; i < kItemFlags; ++i) found[i] = 0;
+    *found = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tensormap(&q_map);
     ptx::prefetch_tensormap(&k_map);
@@ -464,9 +463,9 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         if (!ok) break;
         const bool met = clean_values<C::kSubs, BF16>(smem + C::kOffRing + (v % C::kStages) * C::kBlock, C::kSub,
                                                       max(0, it.clean_from - j * kTile), it.m - j * kTile, lane);
-        // the item's own number, so that nothing has to be reset; the ring
-        // keeps this warp fewer items ahead than there are places
-        if (met) found[items % kItemFlags] = items + 1;
+        // the number of the last such item, however far ahead: an item before
+        // it then looks for values to add back and, where it has none, adds none
+        if (met) *found = items + 1;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(kv_full(v % C::kStages));
@@ -675,7 +674,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         ptx::tc_fence_after();
       }
       const float inv = l > 0.0f ? __fdividef(1.0f, l) : l;       // nothing seen: 0; NaN stays
-      const bool patch = some && found[item % kItemFlags] == item + 1;
+      const bool patch = some && *found > item;
       using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
       T* out = static_cast<T*>(a.out) + (static_cast<int64_t>(it.q0) + row) * a.out_stride + head * D;
 #pragma unroll
