@@ -131,7 +131,8 @@ nvq_status check_kv(const nvq_kv_cache* c, const void* k, int64_t k_stride, cons
   return check_rows(v, rows, width, v_stride, dtype_bytes(dtype));
 }
 
-bool good_scale(float scale) { return scale > 0.0f && scale <= 3.0e38f; }
+// Up to 2^64, so that the factors formed of it stay finite.
+bool good_scale(float scale) { return scale > 0.0f && scale <= 0x1p64f; }
 
 }  // namespace
 

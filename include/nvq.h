@@ -487,7 +487,7 @@ nvq_status nvq_kv_read(const nvq_kv_cache* cache, void* k, int64_t k_stride, voi
  * out   device rows [B, n_heads, head_dim] of `dtype`, out_stride elements
  *       apart: sum_j p_j v_j / sum_j p_j, p_j = exp(scale * q.k_j - max), over
  *       the seq_lens[b] positions of sequence b; zeros where it is 0.
- * scale finite and > 0 (customarily 1/sqrt(head_dim)).
+ * scale > 0 and at most 2^64 (customarily 1/sqrt(head_dim)).
  * Products, softmax statistics and sums are fp32; with NVQ_F32 the operands
  * of the products carry at least 22 bits, with the 16-bit types the
  * probabilities are rounded to tf32 (fp16's significand, fp32's range) for the
@@ -500,7 +500,7 @@ nvq_status nvq_kv_read(const nvq_kv_cache* cache, void* k, int64_t k_stride, voi
  *           Calls that may run at the same time need their own counters and
  *           workspace.  Results do not depend on timing.
  * Errors: as nvq_kv_write, NVQ_ERR_WORKSPACE, NVQ_ERR_INVALID_ARG for a
- * scale that is not finite and positive, NVQ_ERR_BAD_SHAPE when n_heads is no
+ * scale outside (0, 2^64], NVQ_ERR_BAD_SHAPE when n_heads is no
  * multiple of n_kv_heads, B is over 65535, a table row holds 2^31 or more
  * tokens, or all rows' 64-token tiles of every key-value head may pass 2^31.
  */

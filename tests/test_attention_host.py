@@ -113,6 +113,15 @@ def test_prefill_is_refused():
     assert pre(B=0) == OK and pre(tq=0) == OK
 
 
+@pytest.mark.parametrize("call", [lambda **a: dec(cache(), **a), pre])
+def test_scales_whose_factors_would_overflow_are_refused(call):
+    """Up to 2^64; B = 0 returns before anything is launched."""
+    for scale in (float("inf"), 3e38, float(np.nextafter(np.float32(2.0 ** 64), np.float32(np.inf))), -0.1, 0.0):
+        assert call(scale=scale) == ARG and call(scale=scale, B=0) == ARG, scale
+    for scale in (2.0 ** 64, 1.0, 1e-38):
+        assert call(scale=scale, B=0) == OK, scale
+
+
 # --- the binding, on CPU tensors: every check is made before the library is called
 
 def cpu_cache(pages=4, heads=2, page=16, dim=64):

@@ -269,3 +269,25 @@ def test_memory_of_a_call_on_another_stream_is_not_reused_under_it():
     got.append(capi.attn_decode(dev, q, lens, table, cnt, stream=side.cuda_stream))
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for x in got) and not cnt.any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+def test_the_largest_scale_with_equal_scores(dtype):
+    """Queries of zeros: every score is 0 whatever the scale, so the result is
+    the values' mean, not NaN."""
+    page, lens = 16, [5, 70]
+    H, kv, D = 4, 2, 64
+    c = capi.kv_cache(8, kv, page, D)
+    table = torch.tensor([[0, -1, -1, -1, -1], [1, 2, 3, 4, 5]], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 5, 75], dtype=torch.int32, device="cuda")
+    seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ones = torch.ones(75, kv, D, dtype=dtype, device="cuda")
+    capi.kv_write(c, ones, ones, cu, seq, table)
+    want = capi.kv_read(c, cu, seq, table, 75, torch.float32)[1][0, 0, 0].item()
+    q = torch.zeros(2, H, D, dtype=dtype, device="cuda")
+    out = capi.attn_decode(c, q, seq, table, torch.zeros(2 * H, dtype=torch.int32, device="cuda"), scale=2.0 ** 64)
+    # sums of up to 70 equal terms, truncated at each of up to 18 additions (2^-23
+    # each), and the quotient: below 2^-18; fp16 rounds the weights to tf32 and
+    # the result, half a step (2^-11) each
+    tol = 2.0 ** -18 + (0 if dtype == torch.float32 else 2 * 2.0 ** -11)
+    assert ((out.float() - want).abs() <= tol * abs(want)).all()
