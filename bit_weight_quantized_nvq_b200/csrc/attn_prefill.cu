@@ -42,9 +42,9 @@
 // the end.  A warp of its own does it ahead of the products; done by the
 // softmax warps, 2048 tokens of 40 heads took 80 us instead of 71.
 //
-// Measured, cold L2: 8192 tokens, 40 over 8 heads of 128, bf16, causal, 625 us
-// (1100 TFLOP/s; 711 us back to back, at the power limit); 2048 tokens, 40
-// heads, fp16, 67 us.
+// Measured, cold L2: 8192 tokens, 40 over 8 heads of 128, bf16, causal, 625
+// to 640 us by machine (1075 to 1100 TFLOP/s; 710 to 730 back to back, at the
+// power limit); 2048 tokens, 40 heads, fp16, 68 to 70 us.
 #include <algorithm>
 #include <climits>
 #include <mutex>
