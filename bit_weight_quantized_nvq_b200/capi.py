@@ -494,8 +494,9 @@ def attn_decode(cache, q: torch.Tensor, seq_lens: torch.Tensor, block_table: tor
     """Attention of one new token per sequence over the cache
     (nvq_attn_decode): q [B, n_heads, head_dim] float32, float16 or bfloat16;
     returns out of q's shape and type.  counters: device int32
-    [B * n_heads], zero before the first call, left zero; calls that may
-    overlap need their own.  scale: 1/sqrt(head_dim) unless given."""
+    [B * n_heads], zero before the first call, left zero; workspace: contiguous,
+    on q's device, of any type; calls that may overlap need their own of both.
+    scale: 1/sqrt(head_dim) unless given."""
     dt, dev = _dtype(q), q.get_device()
     c = _cache(cache, dev)
     B, cols = seq_lens.shape[0], block_table.shape[-1]
@@ -512,6 +513,8 @@ def attn_decode(cache, q: torch.Tensor, seq_lens: torch.Tensor, block_table: tor
         os_ = _rows("out", out, shape, q, dev)
     if workspace is None:
         workspace = _empty(q, _decode_workspace(dev, B, H, c.n_kv_heads, D), torch.uint8, stream)
+    elif workspace.get_device() != dev or workspace.device.type != q.device.type or not workspace.is_contiguous():
+        raise ValueError(f"workspace: contiguous memory on {q.device} expected, not on {workspace.device}")
     _launch(dev, stream, "nvq_attn_decode", _lib.nvq_attn_decode, c, q.data_ptr(), qs, dt,
             _index("seq_lens", seq_lens, dev, (B,)), _index("block_table", block_table, dev, (B, cols)),
             B, cols, H, D ** -0.5 if scale is None else scale, out.data_ptr(), os_,

@@ -166,3 +166,15 @@ def test_binding_refuses_tensors_that_do_not_fit():
             capi.attn_prefill(*args)
     with pytest.raises(ValueError):
         capi.attn_prefill(x, k, k, i32(3), out=torch.zeros(4, 4, 64, dtype=torch.float16))
+
+
+def test_binding_refuses_a_workspace_elsewhere_or_with_gaps():
+    """The pointer and the size of a workspace stand for memory of the call's
+    device without gaps; anything else is refused before the library is called."""
+    c, q = cpu_cache(), torch.zeros(2, 4, 64)
+    space = torch.zeros(1 << 20, dtype=torch.uint8)
+    for bad in (space[::2], space.view(1024, 1024).t(), torch.zeros(1 << 20, dtype=torch.uint8, device="meta")):
+        with pytest.raises(ValueError, match="workspace"):
+            capi.attn_decode(c, q, i32(2), i32(2, 3), i32(8), workspace=bad)
+    with pytest.raises(ValueError, match="CUDA"):            # what is wrong here is the whole call's device
+        capi.attn_decode(c, q, i32(2), i32(2, 3), i32(8), workspace=space)

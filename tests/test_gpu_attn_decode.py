@@ -291,3 +291,15 @@ def test_the_largest_scale_with_equal_scores(dtype):
     # the result, half a step (2^-11) each
     tol = 2.0 ** -18 + (0 if dtype == torch.float32 else 2 * 2.0 ** -11)
     assert ((out.float() - want).abs() <= tol * abs(want)).all()
+
+
+def test_a_workspace_of_another_device_is_refused():
+    """On the host, before anything is launched."""
+    c = Cache([40], 2, 16, 64, seed=1)
+    q, cnt = queries(1, 4, 64, torch.float16, 1), counters(1, 4)
+    nbytes = capi.lib().nvq_attn_decode_workspace_size(1, 4, 2, 64)
+    for bad in (torch.zeros(nbytes, dtype=torch.uint8), torch.zeros(2 * nbytes, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            capi.attn_decode(c.device(), q, c.dev_lens(), c.dev_table(), cnt, workspace=bad)
+    space = torch.zeros(nbytes // 4, dtype=torch.float32, device="cuda")       # any type
+    compare(c, q, capi.attn_decode(c.device(), q, c.dev_lens(), c.dev_table(), cnt, workspace=space), torch.float16)
