@@ -266,10 +266,10 @@ struct Raw {
 
 // The row as operands: scaled by a power of two so that its largest lies in
 // [2^13, 2^14), then rounded to fp16, and the remainder for `lo`.  Returns
-// the factor that turns the MMA's sums into powers of two; `start` is what the
-// sums over each block begin with, -128 * 2^-24 * sum of the operands.
+// the two factors that turn the MMA's sums into powers of two; `start` is what
+// the sums over each block begin with, -128 * 2^-24 * sum of the operands.
 template <int D, bool F32, bool LO>
-__device__ __forceinline__ float query_row(const Raw<D, F32>& raw, int dtype, float scale_log2,
+__device__ __forceinline__ float2 query_row(const Raw<D, F32>& raw, int dtype, float scale_log2,
                                            uint32_t (&hi)[D / 8], uint32_t (&lo)[D / 8],
                                            float (&start)[D / 32], float (&start_lo)[D / 32]) {
   float x[D / 4], top = 0.0f;
@@ -308,8 +308,14 @@ __device__ __forceinline__ float query_row(const Raw<D, F32>& raw, int dtype, fl
       start_lo[bl] *= -0x1p-17f;
     }
   }
-  // 2^24 (the codes' unit) and 2^-k; k > -128 + 24 even for infinities
-  return scale_log2 * 0x1p24f * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  // 2^24 (the codes' unit) and 2^-k, up to 2^139 (k is -115 and more, even for
+  // infinities): in one factor with the scale only up to 2^40, so that neither
+  // factor overflows for a scale of up to 2^64, nor the product of a sum (below
+  // 2^44 of the codes' units) and the first one.  A sum of 0 stays 0, and a
+  // score is finite where its value is.
+  const int e = 24 - k, e1 = min(e, 40);
+  return make_float2(scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e1) << 23),
+                     __uint_as_float(static_cast<uint32_t>(127 + e - e1) << 23));
 }
 
 template <int D, Rows R>
@@ -536,7 +542,7 @@ attn_decode_kernel(const DecodeArgs a) {
     int rem = clamp_len(a, b) - tile0 * kTile;
     load_queries();
     uint32_t qh[D / 8], ql[D / 8];
-    float factor[kH];
+    float2 factor[kH];
     float start[C::kBlocks], start2[C::kBlocks];       // of rows gq and gq + 8
     factor[0] = query_row<D, R == kSplit, R == kSplit>(raw[0], a.dtype, a.scale_log2, qh, ql, start, start2);
     if constexpr (R == kTwo) {
@@ -615,8 +621,8 @@ attn_decode_kernel(const DecodeArgs a) {
           }
 #pragma unroll
           for (int h = 0; h < kH; ++h) {
-            p[h][2 * x] = sa[h] * factor[h];
-            p[h][2 * x + 1] = sb[h] * factor[h];
+            p[h][2 * x] = sa[h] * factor[h].x * factor[h].y;
+            p[h][2 * x + 1] = sb[h] * factor[h].x * factor[h].y;
           }
         }
         if (valid < 16) {        // the last tile

@@ -303,3 +303,55 @@ def test_a_workspace_of_another_device_is_refused():
             capi.attn_decode(c.device(), q, c.dev_lens(), c.dev_table(), cnt, workspace=bad)
     space = torch.zeros(nbytes // 4, dtype=torch.float32, device="cuda")       # any type
     compare(c, q, capi.attn_decode(c.device(), q, c.dev_lens(), c.dev_table(), cnt, workspace=space), torch.float16)
+
+
+def ladder(n, kv, dim, size, seed):
+    """Keys size * (0.25 .. 1) along one pattern of signs, in no order; the pattern."""
+    rng = np.random.default_rng(seed)
+    sign = rng.choice([-1.0, 1.0], (kv, dim)).astype(np.float32)
+    a = (0.25 + 0.75 * rng.permutation(n) / (n - 1)).astype(np.float32)
+    return torch.from_numpy(size * a[:, None, None] * sign).cuda(), torch.from_numpy(sign).cuda(), torch.from_numpy(a).cuda()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [1e25, 1e36, 3e38])
+def test_the_largest_finite_queries_pick_their_key(dtype, size, dim):
+    """Scores of up to 1e38, apart by 1e22 and more: the value of the largest
+    one alone (of the smallest, for a query of the other sign); its weight is
+    1 and the quotient's divisor 1, so only the result is rounded.  The head
+    beside it keeps its ordinary result."""
+    n, kv = 150, 2
+    k, sign, a = ladder(n, kv, dim, 2.0 ** -5, 3)
+    v = queries(n, kv, dim, torch.float32, 4)
+    c = capi.kv_cache(10, kv, 16, dim)
+    table, cu, ln = torch.arange(10, dtype=torch.int32, device="cuda")[None], cu_of([n]), torch.tensor([n], dtype=torch.int32).cuda()
+    capi.kv_write(c, k, v, cu, ln, table)
+    kd, vd = capi.kv_read(c, cu, ln, table, n, torch.float32)
+    q = torch.empty(1, 3 * kv, dim, dtype=dtype, device="cuda")
+    ordinary = queries(1, kv, dim, dtype, 5)
+    for h in range(kv):
+        q[:, 3 * h], q[:, 3 * h + 1], q[:, 3 * h + 2] = size * sign[h], -size * sign[h], ordinary[:, h]
+    out = capi.attn_decode(c, q, ln, table, counters(1, 3 * kv))
+    half = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8
+    for h in range(kv):
+        for x, pick in ((0, a.argmax()), (1, a.argmin())):
+            assert ((out[0, 3 * h + x].float() - vd[pick, h]).abs() <= half * vd[pick, h].abs()).all()
+    args = [t.double().cpu().numpy() for t in (kd, vd)]
+    ref, aa, e = o.attend_fp64(ordinary.double().cpu().numpy(), *args, dim ** -0.5)
+    tol = bound(ref, aa, e, n, np.abs(args[1]).max(), dtype, torch.float32 if dtype == torch.float32 else "tf32")
+    check(out[:, 2::3], ref, tol)
+
+
+@pytest.mark.parametrize("dtype,size,scale", [
+    (torch.float32, 3e38, None), (torch.float32, 2.0 ** 60, 2.0 ** 64), (torch.bfloat16, 3e38, None),
+    (torch.bfloat16, 2.0 ** 60, 2.0 ** 64), (torch.float16, 65504.0, 2.0 ** 64), (torch.float32, 3e38, 2.0 ** 64)])
+def test_large_queries_at_channels_that_are_zero(dtype, size, scale):
+    """Every score is 0, however large the factors around it are: the mean of the values."""
+    lens, kv, dim = [70, 5], 2, 128
+    c = Cache(lens, kv, 16, dim, seed=6)
+    c.codes[0][..., 40:44] = 0
+    q = torch.zeros(2, 6, dim, dtype=dtype, device="cuda")
+    q[..., 40:44] = size
+    out = capi.attn_decode(c.device(), q, c.dev_lens(), c.dev_table(), counters(2, 6), scale=scale)
+    compare(c, q, out, dtype, scale)
