@@ -65,6 +65,10 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kUnitCost = 3;         // a unit's start and end, in tiles
 constexpr int kFlush = 4;            // tiles between additions of the accumulators, with fp32
 constexpr float kLazy = 8.0f;        // the running maximum may lag by this power of two
+// The running maximum before any finite score: a finite number, so that a
+// score of -infinity (its value is below fp32's range) gets the weight 0
+// where no finite one came before it, instead of exp2(-inf - -inf).
+constexpr float kNone = -3.402823466e38f;
 
 // How the 16 rows of an MMA are used: fp32 heads as hi (rows 0-7) and lo
 // (rows 8-15); up to 8 heads of a 16-bit type; up to 16 of them.
@@ -513,8 +517,7 @@ attn_decode_kernel(const DecodeArgs a) {
       float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < kWarps; ++x) {
-        const float mx = ml[2 * (x * C::kHeads + hn)];
-        const float c = mx == -INFINITY ? 0.0f : exp2_approx(mx - top);
+        const float c = exp2_approx(ml[2 * (x * C::kHeads + hn)] - top);
         L = fmaf(c, ml[2 * (x * C::kHeads + hn) + 1], L);
         const float4 v = *red(x, h, d4);
         O.x = fmaf(c, v.x, O.x), O.y = fmaf(c, v.y, O.y), O.z = fmaf(c, v.z, O.z), O.w = fmaf(c, v.w, O.w);
@@ -559,7 +562,7 @@ attn_decode_kernel(const DecodeArgs a) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
 #pragma unroll
-    for (int h = 0; h < kH; ++h) m[h] = -INFINITY, l[h] = 0.0f;
+    for (int h = 0; h < kH; ++h) m[h] = kNone, l[h] = 0.0f;
 
     // The tensor core adds to its accumulators by truncation, so with fp32 they
     // hold kFlush tiles at a time and are added up here (131072 tokens: 2.6e-6
@@ -809,12 +812,12 @@ attn_decode_kernel(const DecodeArgs a) {
           float mn = top;
 #pragma unroll
           for (int u = 0; u < 8; ++u) mn = fmaxf(mn, y[u].x);
-          const float c = top == -INFINITY ? 0.0f : exp2_approx(top - mn);
+          const float c = exp2_approx(top - mn);      // mn is at least kNone: k0 is a part
           top = mn;
           L *= c, O.x *= c, O.y *= c, O.z *= c, O.w *= c;
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const float f = y[u].x == -INFINITY ? 0.0f : exp2_approx(y[u].x - mn);
+            const float f = exp2_approx(y[u].x - mn);
             L = fmaf(f, y[u].y, L);
             O.x = fmaf(f, v[u].x, O.x), O.y = fmaf(f, v[u].y, O.y), O.z = fmaf(f, v[u].z, O.z), O.w = fmaf(f, v[u].w, O.w);
           }

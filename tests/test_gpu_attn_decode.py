@@ -355,3 +355,29 @@ def test_large_queries_at_channels_that_are_zero(dtype, size, scale):
     q[..., 40:44] = size
     out = capi.attn_decode(c.device(), q, c.dev_lens(), c.dev_table(), counters(2, 6), scale=scale)
     compare(c, q, out, dtype, scale)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dim,group", [(64, 1), (128, 1), (128, 16)])
+@pytest.mark.parametrize("n,finite", [(200, range(190, 200)), (200, range(0, 3)), (200, [77]), (20000, [19990, 19999]),
+                                      (20000, [5, 9000]), (20000, range(0, 20000, 1000))])
+def test_scores_below_the_range_count_for_nothing(dtype, dim, group, n, finite):
+    """Scores under -3.4e38 in every tile, warp or part but some: weights of 0
+    against the scores of 0 beside them, whose values' mean is the result."""
+    kv = 2
+    k = torch.full((n, kv, dim), -60000.0, device="cuda")
+    finite = list(finite)
+    k[finite] = 0
+    v = queries(n, kv, dim, torch.float32, 1)
+    pages = -(-n // 64)
+    c = capi.kv_cache(pages, kv, 64, dim)
+    table, cu, ln = torch.arange(pages, dtype=torch.int32, device="cuda")[None], cu_of([n]), torch.tensor([n], dtype=torch.int32).cuda()
+    capi.kv_write(c, k, v, cu, ln, table)
+    vd = capi.kv_read(c, cu, ln, table, n, torch.float32)[1][finite].double().cpu().numpy()
+    q = torch.full((1, kv * group, dim), 3e38, dtype=dtype, device="cuda")
+    out = capi.attn_decode(c, q, ln, table, counters(1, kv * group))
+    zero = np.zeros((1, kv * group, dim))
+    ref, a, e = o.attend_fp64(zero, np.zeros_like(vd), vd, dim ** -0.5)
+    tol = bound(ref, a, e, n, np.abs(vd).max(), dtype, torch.float32 if dtype == torch.float32 else "tf32")
+    check(out, ref, tol)
+    assert capi.error_flags() == 0
