@@ -26,12 +26,15 @@
 // Each warp issuing TMA boxes of its own: 174 us for the 706 MB, against 156.)
 //
 // Scores (m16n8k16, fp16 operands): A holds the queries, B the codes of 8
-// tokens, which are exact in
-// fp16 (as code + 128, the bias coming off in fp32).  Each query row is scaled by a power of
-// two to just below 2^14 before it is rounded, so 16-bit queries are exact
-// and fp32 ones become an exact pair hi + lo of at least 22 bits, in rows g and
-// g + 8 of the same fragment.  Two MMAs cover one block of 32 values; its
-// scale is then applied in fp32.
+// tokens, which are exact in fp16.  (As code + 128, without the subtraction
+// that takes the 128 off again, the partial sums were as large as 128 sum |q|
+// whatever the codes: with one large key channel per block, at which the query
+// is 0, fp32 results were off by up to 4 times their bound.)  Each query row
+// is scaled by a power of two to just below 2^14 before it is rounded, so
+// 16-bit queries are exact and fp32 ones become a pair hi + lo of at least 22
+// bits, in rows g and g + 8 of the same fragment (both down to 2^-39 of the
+// row's largest element).  Two MMAs cover one block of 32 values; its scale is
+// then applied in fp32.
 //
 // Values (m16n8k8, tf32 operands), transposed, o^T = V^T p^T: A holds 16 dims of
 // 8 tokens, exact, B = p_j * scale_j of 8 heads, in tf32 because the scales
@@ -193,13 +196,13 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   return v;
 }
 
-// Four int8 codes as fp16 (u = code + 128 per byte): 0x00bb is u * 2^-24, the
-// subnormals and the first binade being evenly spaced, and tensor cores
-// take them exactly.  The bias comes off through the accumulator's start.
+// Four int8 codes as fp16 (u = code + 128 per byte): 0x64bb is 1024 + u, and
+// 1152 off it is exact.
 __device__ __forceinline__ void codes_to_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
   const uint32_t u = w ^ 0x80808080u;
-  lo = __byte_perm(u, 0u, 0x4140);
-  hi = __byte_perm(u, 0u, 0x4342);
+  const __half2 off = dev::bits_h2(0x64806480u);
+  lo = dev::h2_bits(__hsub2(dev::bits_h2(__byte_perm(u, 0x64646464u, 0x4140)), off));
+  hi = dev::h2_bits(__hsub2(dev::bits_h2(__byte_perm(u, 0x64646464u, 0x4342)), off));
 }
 // The same as fp32: 0x4B0000bb is 2^23 + u.  The differences are exact.
 __device__ __forceinline__ void codes_to_f32(uint32_t w, uint32_t (&f)[4]) {
@@ -270,12 +273,10 @@ struct Raw {
 
 // The row as operands: scaled by a power of two so that its largest lies in
 // [2^13, 2^14), then rounded to fp16, and the remainder for `lo`.  Returns
-// the two factors that turn the MMA's sums into powers of two; `start` is what
-// the sums over each block begin with, -128 * 2^-24 * sum of the operands.
+// the two factors that turn the MMA's sums into powers of two.
 template <int D, bool F32, bool LO>
 __device__ __forceinline__ float2 query_row(const Raw<D, F32>& raw, int dtype, float scale_log2,
-                                           uint32_t (&hi)[D / 8], uint32_t (&lo)[D / 8],
-                                           float (&start)[D / 32], float (&start_lo)[D / 32]) {
+                                           uint32_t (&hi)[D / 8], uint32_t (&lo)[D / 8]) {
   float x[D / 4], top = 0.0f;
   raw.values(dtype, x);
 #pragma unroll
@@ -286,40 +287,22 @@ __device__ __forceinline__ float2 query_row(const Raw<D, F32>& raw, int dtype, f
   const int k = min(126, 140 - static_cast<int>(__float_as_uint(top) >> 23));
   const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
 #pragma unroll
-  for (int bl = 0; bl < D / 32; ++bl) {
-    start[bl] = 0.0f;
-    if (LO) start_lo[bl] = 0.0f;
-#pragma unroll
-    for (int i = 4 * bl; i < 4 * bl + 4; ++i) {
-      const float u = x[2 * i] * up, v = x[2 * i + 1] * up;
-      const __half2 h = __floats2half2_rn(u, v);
-      const float2 f = __half22float2(h);
-      hi[i] = dev::h2_bits(h);
-      start[bl] += f.x + f.y;
-      if (LO) {
-        const __half2 r = __floats2half2_rn(u - f.x, v - f.y);
-        const float2 rf = __half22float2(r);
-        lo[i] = dev::h2_bits(r);
-        start_lo[bl] += rf.x + rf.y;
-      }
-    }
-    start[bl] += __shfl_xor_sync(0xffffffffu, start[bl], 1);
-    start[bl] += __shfl_xor_sync(0xffffffffu, start[bl], 2);
-    start[bl] *= -0x1p-17f;
+  for (int i = 0; i < D / 8; ++i) {
+    const float u = x[2 * i] * up, v = x[2 * i + 1] * up;
+    const __half2 h = __floats2half2_rn(u, v);
+    hi[i] = dev::h2_bits(h);
     if (LO) {
-      start_lo[bl] += __shfl_xor_sync(0xffffffffu, start_lo[bl], 1);
-      start_lo[bl] += __shfl_xor_sync(0xffffffffu, start_lo[bl], 2);
-      start_lo[bl] *= -0x1p-17f;
+      const float2 f = __half22float2(h);
+      lo[i] = dev::h2_bits(__floats2half2_rn(u - f.x, v - f.y));
     }
   }
-  // 2^24 (the codes' unit) and 2^-k, up to 2^139 (k is -115 and more, even for
-  // infinities): in one factor with the scale only up to 2^40, so that neither
-  // factor overflows for a scale of up to 2^64, nor the product of a sum (below
-  // 2^44 of the codes' units) and the first one.  A sum of 0 stays 0, and a
-  // score is finite where its value is.
-  const int e = 24 - k, e1 = min(e, 40);
+  // 2^-k is up to 2^115, even for infinities: in one factor with the scale only
+  // up to 2^16, so that neither factor overflows for a scale of up to 2^64, nor
+  // the product of a sum (below 2^44) and the first one.  A sum of 0 stays 0,
+  // and a score is finite where its value is.
+  const int e1 = min(-k, 16);
   return make_float2(scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e1) << 23),
-                     __uint_as_float(static_cast<uint32_t>(127 + e - e1) << 23));
+                     __uint_as_float(static_cast<uint32_t>(127 - k - e1) << 23));
 }
 
 template <int D, Rows R>
@@ -546,12 +529,10 @@ attn_decode_kernel(const DecodeArgs a) {
     load_queries();
     uint32_t qh[D / 8], ql[D / 8];
     float2 factor[kH];
-    float start[C::kBlocks], start2[C::kBlocks];       // of rows gq and gq + 8
-    factor[0] = query_row<D, R == kSplit, R == kSplit>(raw[0], a.dtype, a.scale_log2, qh, ql, start, start2);
+    factor[0] = query_row<D, R == kSplit, R == kSplit>(raw[0], a.dtype, a.scale_log2, qh, ql);
     if constexpr (R == kTwo) {
       uint32_t none[D / 8];
-      float unused[C::kBlocks];
-      factor[kH - 1] = query_row<D, false, false>(raw[kH - 1], a.dtype, a.scale_log2, ql, none, start2, unused);
+      factor[kH - 1] = query_row<D, false, false>(raw[kH - 1], a.dtype, a.scale_log2, ql, none);
     }
 
     // o[n][2 * bl + x]: heads 8 n + 2 j (elements 0, 2) and 8 n + 2 j + 1 (1, 3),
@@ -610,8 +591,7 @@ attn_decode_kernel(const DecodeArgs a) {
             codes_to_h2(c8.y, b2, b3);
             float acc[4];
             const uint32_t z = 0;
-            const float c = start[bl], c2 = R == kOne ? 0.0f : start2[bl];
-            mma_f16(acc, qh[4 * bl], R == kOne ? z : ql[4 * bl], qh[4 * bl + 1], R == kOne ? z : ql[4 * bl + 1], b0, b1, c, c, c2, c2);
+            mma_f16(acc, qh[4 * bl], R == kOne ? z : ql[4 * bl], qh[4 * bl + 1], R == kOne ? z : ql[4 * bl + 1], b0, b1, 0.0f, 0.0f, 0.0f, 0.0f);
             mma_f16(acc, qh[4 * bl + 2], R == kOne ? z : ql[4 * bl + 2], qh[4 * bl + 3], R == kOne ? z : ql[4 * bl + 3], b2, b3,
                     acc[0], acc[1], acc[2], acc[3]);
             if (R == kSplit) acc[0] += acc[2], acc[1] += acc[3];

@@ -131,7 +131,7 @@ nvq_status check_kv(const nvq_kv_cache* c, const void* k, int64_t k_stride, cons
   return check_rows(v, rows, width, v_stride, dtype_bytes(dtype));
 }
 
-// Up to 2^64: what the kernels multiply it with before the scores (2^41 at most)
+// Up to 2^64: what the kernels multiply it with before the scores (2^17 at most)
 // leaves it finite.
 bool good_scale(float scale) { return scale > 0.0f && scale <= 0x1p64f; }
 

@@ -381,3 +381,23 @@ def test_scores_below_the_range_count_for_nothing(dtype, dim, group, n, finite):
     tol = bound(ref, a, e, n, np.abs(vd).max(), dtype, torch.float32 if dtype == torch.float32 else "tf32")
     check(out, ref, tol)
     assert capi.error_flags() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim,group", [(128, 8), (64, 2), (128, 12)])
+def test_blocks_with_one_large_channel(dtype, dim, group):
+    """Key blocks whose scale comes from one channel, at which the query is 0:
+    the other codes are 0 or 1, and a score keeps the precision that its own
+    products have.  Few keys, so that an error of one shows."""
+    lens, kv = [2, 3, 5, 40, 2, 2], 4
+    c = Cache(lens, kv, 16, dim, seed=11)
+    rng = np.random.default_rng(4)
+    c.codes[0] = rng.choice([-1, 0, 1], c.codes[0].shape, p=[0.03, 0.94, 0.03])
+    c.codes[0][..., ::32] = rng.choice([-127, 127], c.codes[0][..., ::32].shape)
+    for b, n in enumerate(lens):
+        pos = np.arange(n)
+        c.scales[0][c.table[b, pos // 16], :, pos % 16] = 8.0
+    q = queries(len(lens), kv * group, dim, dtype, 7).abs()
+    q[..., ::32] = 0
+    out = capi.attn_decode(c.device(), q, c.dev_lens(), c.dev_table(), counters(len(lens), kv * group))
+    compare(c, q, out, dtype)
