@@ -549,6 +549,7 @@ attn_decode_kernel(const DecodeArgs a) {
     // hold kFlush tiles at a time and are added up here (131072 tokens: 2.6e-6
     // of error without it).
     float sum[R == kSplit ? D / 16 : 1][4] = {};
+    uint32_t odd = 0;             // fp16 pair: the largest |value scale| seen by this lane
     for (int t = n_here; t > 0; --t, rem -= kTile) {
       if (R == kSplit && (n_here - t) % kFlush == kFlush - 1) {
 #pragma unroll
@@ -652,6 +653,11 @@ attn_decode_kernel(const DecodeArgs a) {
           }
         }
         // ---- values: one block of 32 at a time
+        if constexpr (R != kSplit) {
+          // one word of them a lane: the largest |scale| of its two blocks
+          uint32_t w = 4 * lane < C::kScales && 2 * lane / C::kBlocks < valid ? lds32(vsb + 4 * lane) : 0u;
+          odd = __vmaxu2(odd, w & 0x7FFF7FFFu);
+        }
         uint2 sc[4];     // the tokens' value scales
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -677,7 +683,11 @@ attn_decode_kernel(const DecodeArgs a) {
                 hi[h][i] = __float_as_uint(x) & 0xFFFFE000u;              // tf32, exactly
                 lo[i] = __float_as_uint(x - __uint_as_float(hi[h][i]));
               } else {
-                hi[h][i] = __float_as_uint(x) + 0x1000u;                  // to nearest: the MMA drops 13 bits
+                // to nearest: the MMA drops 13 bits.  A NaN's carry goes into
+                // its sign; `odd` brings it back at the unit's end (64
+                // sequences of 2048..8192: 156 us without it, 158 with it, 162
+                // with cvt.rna here)
+                hi[h][i] = __float_as_uint(x) + 0x1000u;
               }
             }
           }
@@ -708,6 +718,25 @@ attn_decode_kernel(const DecodeArgs a) {
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int u = 0; u < 4; ++u) o[0][i][u] += sum[i][u];
+    }
+    if constexpr (R != kSplit) {
+      // A value block with a NaN scale gives NaN; with an infinite one what it
+      // is, but NaN where its weight underflowed
+      if (__any_sync(0xffffffffu, __vcmpgeu2(odd, 0x7C007C00u) != 0)) {
+#pragma unroll
+        for (int i = C::kBlocks / 2; i < 32; i <<= 1) odd = __vmaxu2(odd, __shfl_xor_sync(0xffffffffu, odd, i));
+#pragma unroll
+        for (int bl = 0; bl < C::kBlocks; ++bl) {
+          const uint32_t top = (__shfl_sync(0xffffffffu, odd, bl / 2) >> (16 * (bl & 1))) & 0xFFFFu;
+#pragma unroll
+          for (int n = 0; n < kH; ++n)
+#pragma unroll
+            for (int i = 2 * bl; i < 2 * bl + 2; ++i)
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (top > 0x7C00u || (top == 0x7C00u && fabsf(o[n][i][u]) < INFINITY)) o[n][i][u] = __uint_as_float(0x7FFFFFFFu);
+        }
+      }
     }
     // ------------------ the four warps' parts of the unit, joined ------------------
     // Eight heads at a time.  A part goes to this CTA's slot of the workspace:

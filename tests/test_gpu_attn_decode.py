@@ -401,3 +401,29 @@ def test_blocks_with_one_large_channel(dtype, dim, group):
     q[..., ::32] = 0
     out = capi.attn_decode(c.device(), q, c.dev_lens(), c.dev_table(), counters(len(lens), kv * group))
     compare(c, q, out, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim,group", [(128, 4), (64, 2), (128, 16)])
+def test_value_blocks_that_are_not_finite_are_seen(dtype, dim, group):
+    """A NaN or infinite scale of a value block makes that block's results NaN or
+    infinite in every head, whatever the weight of its key, a weight that
+    underflows included; the other blocks and sequences keep their bits."""
+    c = Cache([100, 20], 2, 16, dim, seed=9)
+    B, H = 2, 2 * group
+    for spread in (1.0, 300.0):                       # 300: most weights are 0
+        q = queries(B, H, dim, dtype, 3, spread)
+        run = lambda: capi.attn_decode(c.device(), q, c.dev_lens(), c.dev_table(), counters(B, H))
+        clean = run()
+        for pos, head, bad in ((0, 0, np.nan), (99, 1, np.nan), (50, 1, np.inf), (77, 0, -np.nan)):
+            pg, off = c.table[0, pos // 16], pos % 16
+            keep = c.scales[1][pg, head, off, 1]
+            c.scales[1][pg, head, off, 1] = bad
+            out = run()
+            c.scales[1][pg, head, off, 1] = keep
+            hit = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+            hit[0, head * group:(head + 1) * group, 32:64] = True
+            assert torch.equal(out[~hit], clean[~hit]), (pos, bad, spread)
+            assert not torch.isfinite(out[hit]).any(), (pos, bad, spread)
+            if bad != bad:
+                assert torch.isnan(out[hit]).all()
