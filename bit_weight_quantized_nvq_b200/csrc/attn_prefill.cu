@@ -636,6 +636,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
           sum = large ? form(Yes{}) : form(No{});
           const bool grow = !(sum <= kLazy);
           if (round > 0 || !__any_sync(0xffffffffu, grow)) break;
+          ptx::tmem_wait_st();       // stores to one place are not kept in order by themselves
           const float top = largest();
           const float f = grow ? exp2_approx((ref - top) * c) : 1.0f;
           if (grow) ref = top;

@@ -313,3 +313,25 @@ def test_a_long_call_with_unseen_keys_only_at_its_end():
     # equal scores and values: the sums are whole numbers up to 2^24, exact
     assert (out[:n[0]] == 1).all()
     compare(q[n[0]:], k[m[0]:], v[m[0]:], n[1:], m[1:], out[n[0]:], torch.bfloat16, False)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_steps_formed_twice_repeat_their_bits(dtype, dim):
+    """Every step of 64 keys passes the mark of the one before it for some rows
+    of each warp, and the first step has infinite scores for some: the
+    probabilities are written twice, and the second ones count, each time."""
+    n = 500
+    q, k, v = rows(n, 2, dim, dtype, 1), rows(n, 1, dim, dtype, 2), rows(n, 1, dim, dtype, 3)
+    steps = torch.arange(n, device="cuda").div(64, rounding_mode="floor").view(-1, 1).to(dtype)
+    q[..., 0] = torch.where(torch.arange(n, device="cuda") % 3 == 0, 1.0, 0.0).view(-1, 1).to(dtype)
+    k[..., 0] = 40 * steps
+    want = capi.attn_prefill(q, k, v, cu_of([n]), scale=0.5)
+    compare(q, k, v, [n], [n], want, dtype, True, 0.5)
+    kk = k.clone()
+    kk[5, 0, 1] = float("inf")
+    odd = capi.attn_prefill(q, kk, v, cu_of([n]), scale=0.5)
+    for _ in range(20):
+        assert torch.equal(capi.attn_prefill(q, k, v, cu_of([n]), scale=0.5), want)
+        got = capi.attn_prefill(q, kk, v, cu_of([n]), scale=0.5)
+        assert torch.equal(got.view(torch.int16), odd.view(torch.int16))
