@@ -29,8 +29,8 @@
 // items are (sequence, tile, heads), the later tiles of a sequence (more
 // keys) first, dealt to the CTAs forwards and backwards in turn.
 //
-// The running maximum is a reference point only: the first step's maximum,
-// kept while no later step's exponentials add up to more than 2^8 (then none of
+// The running maximum is a reference point only: the maximum of the first step
+// with a finite score, kept while no later step's exponentials add up to more than 2^8 (then none of
 // them is above that).  So a step costs no search for its maximum and no
 // rescaling of O; where a row passes the mark, its warp searches, waits for the
 // product before, rescales O and forms the step again.
@@ -567,6 +567,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
       const int steps = s ? it.steps[1] : it.steps[0], head = s ? it.head[1] : it.head[0];
       const int limit = it.limit(row, a.causal);
       float ref = 0.0f, l = 0.0f;                  // reference (a score); sum
+      bool fresh = limit > 0;                      // no reference yet
       for (int i = 0; ok && i < steps; ++i) {
         const int b = i & 1;
         ok = warp_wait(s_full(s, b), (s_par >> b) & 1);
@@ -599,9 +600,13 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
             top[e / 2 % 4] = max3_nan(top[e / 2 % 4], __uint_as_float(v[e / 32][e % 32]), __uint_as_float(v[e / 32][e % 32 + 1]));
           return max3_nan(max3_nan(top[0], top[1], top[2]), top[3], top[3]);
         };
-        if (i == 0) {
+        // the first step with a score above -infinity has a row's reference
+        if (__any_sync(0xffffffffu, fresh)) {
           const float top = largest();
-          if (fabsf(top) < INFINITY) ref = top;
+          if (fresh && !(top == -INFINITY)) {
+            if (fabsf(top) < INFINITY) ref = top;
+            fresh = false;
+          }
         }
         // The exponentials against the reference, and their sum.  Where scores
         // are large the difference comes first: it is exact near the maximum.

@@ -335,3 +335,26 @@ def test_steps_formed_twice_repeat_their_bits(dtype, dim):
         assert torch.equal(capi.attn_prefill(q, k, v, cu_of([n]), scale=0.5), want)
         got = capi.attn_prefill(q, kk, v, cu_of([n]), scale=0.5)
         assert torch.equal(got.view(torch.int16), odd.view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hidden", [1, 64, 130])
+@pytest.mark.parametrize("low", [0.0, -12.0, -20.0, -200.0])
+def test_a_first_step_of_infinite_scores(dtype, dim, hidden, low):
+    """The first keys score -infinity, like hidden ones, and the later scores
+    lie far below 0: the reference comes from them.  Behind 1, 64 and 130 such
+    keys; the rows before them have no finite score, which is the formula's
+    0 / 0 and is not looked at."""
+    n = 300
+    q, k, v = rows(n, 2, dim, dtype, 1), rows(n, 1, dim, dtype, 2), rows(n, 1, dim, dtype, 3)
+    q[..., 0], k[..., 0] = 1.0, low
+    kk = k.clone()
+    kk[:hidden, 0, 0] = float("-inf")
+    out = capi.attn_prefill(q, kk, v, cu_of([n]), scale=1.0)
+    torch.cuda.synchronize()
+    args = [x.double().cpu().numpy() for x in (q, k, v)]
+    for i in (hidden, hidden + 1, 140, 191, 299):
+        kh, vh = (x[hidden:i + 1] for x in args[1:])
+        ref, a, e = o.attend_fp64(args[0][i:i + 1], kh, vh, 1.0)
+        check(out[i:i + 1], ref, bound(ref, a, e, i + 1, np.abs(vh).max(), dtype, dtype), f"row {i}")
