@@ -238,11 +238,6 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   F2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -608,18 +603,21 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
             fresh = false;
           }
         }
-        // The exponentials against the reference, and their sum.  Where scores
-        // are large the difference comes first: it is exact near the maximum.
+        // The exponentials against the reference, and their sum.  Where a row's
+        // scores are large the difference comes first: it is exact near the
+        // maximum.  Each row goes by its own reference (fma(x + -0, c, n) is
+        // fma(x, c, n)), so that no other row of the warp changes its bits.
         auto form = [&](auto large) -> float {
           F2 sum0 = f2(0.0f), sum1 = f2(0.0f);
-          const F2 n2 = decltype(large)::value ? f2(-ref) : f2(-ref * c), c2 = f2(c);
+          const bool own = decltype(large)::value && fabsf(ref * c) > kLarge;
+          const F2 m2 = f2(own ? -ref : -0.0f), n2 = f2(own ? 0.0f : -ref * c), c2 = f2(c);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t p[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const F2 x = f2(__uint_as_float(v[h][e]), __uint_as_float(v[h][e + 1]));
-              const float2 u = split2(decltype(large)::value ? mul2(add2(x, n2), c2) : fma2(x, c2, n2));
+              const float2 u = split2(fma2(decltype(large)::value ? add2(x, m2) : x, c2, n2));
               const float2 y = make_float2(exp2_approx(u.x), exp2_approx(u.y));
               (e & 2 ? sum1 : sum0) = add2(e & 2 ? sum1 : sum0, f2(y.x, y.y));
               p[e / 2] = pack2<BF16>(y.x, y.y);
@@ -634,11 +632,9 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         // No exponential is above their sum: while that stays below 2^8 the
         // reference may lag.  Else (NaN among them) the step's maximum becomes
         // the reference, and the step is formed again.
-        bool large = false;
         float sum;
         for (int round = 0;; ++round) {
-          large |= __any_sync(0xffffffffu, fabsf(ref * c) > kLarge);
-          sum = large ? form(Yes{}) : form(No{});
+          sum = __any_sync(0xffffffffu, fabsf(ref * c) > kLarge) ? form(Yes{}) : form(No{});
           const bool grow = !(sum <= kLazy);
           if (round > 0 || !__any_sync(0xffffffffu, grow)) break;
           ptx::tmem_wait_st();       // stores to one place are not kept in order by themselves

@@ -358,3 +358,40 @@ def test_a_first_step_of_infinite_scores(dtype, dim, hidden, low):
         kh, vh = (x[hidden:i + 1] for x in args[1:])
         ref, a, e = o.attend_fp64(args[0][i:i + 1], kh, vh, 1.0)
         check(out[i:i + 1], ref, bound(ref, a, e, i + 1, np.abs(vh).max(), dtype, dtype), f"row {i}")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_large_scores_of_other_rows_change_no_bit(dtype, dim):
+    """One key with a score of thousands, or an infinite one, for the rows that
+    see it: the rows before it, in the same warps and steps, keep their bits.
+    So does a sequence whose neighbour behind it has large queries, which lie
+    in the same tile's rows."""
+    n = 200
+    q, k, v = rows(n, 2, dim, dtype, 1), rows(n, 1, dim, dtype, 2), rows(n, 1, dim, dtype, 3)
+    clean = capi.attn_prefill(q, k, v, cu_of([n]))
+    for at in (90, 7, 127):
+        for big in (2000.0, 30000.0, float("inf")):
+            kk = k.clone()
+            kk[at] = big * q[at, :1].sign()
+            out = capi.attn_prefill(q, kk, v, cu_of([n]))
+            assert torch.equal(out[:at], clean[:at]), (at, big)
+            assert not torch.equal(out[at:], clean[at:])
+    both = [77, 123]
+    want = capi.attn_prefill(q, k, v, cu_of(both))
+    for gain in (1e3, 1e4):
+        qq = q.clone()
+        qq[77:] *= gain
+        out = capi.attn_prefill(qq, k, v, cu_of(both))
+        assert torch.equal(out[:77], want[:77]) and not torch.equal(out[77:], want[77:])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_large_and_small_scores_in_one_warp(dtype):
+    """Rows with scores of thousands between rows with ordinary ones."""
+    n, dim = 300, 128
+    q, k, v = rows(n, 2, dim, dtype, 1), rows(n, 1, dim, dtype, 2), rows(n, 1, dim, dtype, 3)
+    q[::3, :, 0], k[..., 0] = 60.0, 100.0
+    q[1::3, :, 0] = -60.0
+    out = capi.attn_prefill(q, k, v, cu_of([n]), scale=0.5)
+    compare(q, k, v, [n], [n], out, dtype, True, 0.5)
