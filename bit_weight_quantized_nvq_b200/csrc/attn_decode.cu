@@ -122,7 +122,7 @@ struct Walk {
 };
 
 __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int b) {
-  return max(0, min(__ldg(a.lens + b), a.max_pages * a.page));
+  return max(0, min(a.lens[b], a.max_pages * a.page));
 }
 __device__ __forceinline__ int tiles_of(const DecodeArgs& a, int b) {
   return static_cast<int>((clamp_len(a, b) + int64_t{kTile - 1}) / kTile);
@@ -245,10 +245,10 @@ struct Raw {
     for (int bl = 0; bl < D / 32; ++bl) {
       if (F32) {
         const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(q) + at + 32 * bl + 8 * j);
-        w[2 * bl] = on ? __ldg(s) : make_uint4(0, 0, 0, 0);
-        w[(2 * bl + 1) % (sizeof(w) / 16)] = on ? __ldg(s + 1) : make_uint4(0, 0, 0, 0);
+        w[2 * bl] = on ? *s : make_uint4(0, 0, 0, 0);
+        w[(2 * bl + 1) % (sizeof(w) / 16)] = on ? s[1] : make_uint4(0, 0, 0, 0);
       } else {
-        w[bl] = on ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(q) + at + 32 * bl + 8 * j))
+        w[bl] = on ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(q) + at + 32 * bl + 8 * j)
                    : make_uint4(0, 0, 0, 0);
       }
     }
@@ -394,7 +394,7 @@ attn_decode_kernel(const DecodeArgs a) {
     p_off = pos0 % a.page;
     p_head = pw.unit / a.chunks;
     p_table = a.table + static_cast<int64_t>(pw.b) * a.max_pages;
-    if (p_rem > 0) p_page = __ldg(p_table + p_idx);
+    if (p_rem > 0) p_page = p_table[p_idx];
   };
   auto issue = [&]() {
     if (p_left > 0) {
@@ -429,7 +429,7 @@ attn_decode_kernel(const DecodeArgs a) {
           p_off -= a.page;
           ++p_idx;
         }
-        if (p_rem > 0) p_page = __ldg(p_table + p_idx);
+        if (p_rem > 0) p_page = p_table[p_idx];
       } else {
         Walk pw = pw_s[warp];
         next_unit(a, pw, U);
@@ -459,7 +459,7 @@ attn_decode_kernel(const DecodeArgs a) {
 
   // sequences without tokens: zeros
   for (int b = cta; b < a.B; b += G) {
-    const int64_t len = __ldg(a.lens + b);
+    const int64_t len = a.lens[b];
     if (threadIdx.x == 0 && (len < 0 || len > static_cast<int64_t>(a.max_pages) * a.page))
       atomicOr(&g_attn_decode_error_flags, 2u);
     if (clamp_len(a, b) == 0) {

@@ -111,9 +111,9 @@ struct Item {
 };
 
 __device__ __forceinline__ void sequence(const Args& a, int b, int& q0, int& n, int& k0, int& m) {
-  q0 = __ldg(a.cu_q + b);
-  int q1 = __ldg(a.cu_q + b + 1), k1 = __ldg(a.cu_k + b + 1);
-  k0 = __ldg(a.cu_k + b);
+  q0 = a.cu_q[b];
+  int q1 = a.cu_q[b + 1], k1 = a.cu_k[b + 1];
+  k0 = a.cu_k[b];
   if (q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k) {
     // no keys; the rows that lie inside give zeros
     atomicOr(&g_attn_prefill_error_flags, 2u);

@@ -44,12 +44,12 @@ struct Paged {
 __device__ __forceinline__ int64_t warp_place(const Paged& p, int row, int lane) {
   const int b = dev::warp_find_seq(p.cu, p.B, row, lane);
   if (b >= p.B) return -1;
-  const int64_t pos = static_cast<int64_t>(__ldg(p.lens + b)) - __ldg(p.cu + b + 1) + row;
+  const int64_t pos = static_cast<int64_t>(p.lens[b]) - p.cu[b + 1] + row;
   int page = -1, off = 0;
   if (pos >= 0 && pos < static_cast<int64_t>(p.max_pages) * p.page) {
     const int col = static_cast<int>(static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page));   // a length is below 2^31
     off = static_cast<int>(pos) - col * p.page;
-    page = __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + col);
+    page = p.table[static_cast<int64_t>(b) * p.max_pages + col];
   }
   if (page < 0 || page >= p.n_pages) {
     if (lane == 0) atomicOr(&g_kv_error_flags, 2u);
@@ -121,9 +121,8 @@ __device__ __forceinline__ void quantise(const float (&f)[N], float d32, uint32_
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-kv_write_kernel(const Paged p, const T* __restrict__ k, int64_t k_stride,
-                const T* __restrict__ v, int64_t v_stride, int8_t* __restrict__ kc,
-                __half* __restrict__ ks, int8_t* __restrict__ vc, __half* __restrict__ vs) {
+kv_write_kernel(const Paged p, const T* k, int64_t k_stride, const T* v, int64_t v_stride,
+                int8_t* kc, __half* ks, int8_t* vc, __half* vs) {
   constexpr int N = Share<T>::kElems, kLanes = 32 / N;      // lanes of a Q8_0 block
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -171,9 +170,8 @@ kv_write_kernel(const Paged p, const T* __restrict__ k, int64_t k_stride,
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-kv_read_kernel(const Paged p, const int8_t* __restrict__ kc, const __half* __restrict__ ks,
-               const int8_t* __restrict__ vc, const __half* __restrict__ vs, T* __restrict__ k,
-               int64_t k_stride, T* __restrict__ v, int64_t v_stride) {
+kv_read_kernel(const Paged p, const int8_t* kc, const __half* ks, const int8_t* vc,
+               const __half* vs, T* k, int64_t k_stride, T* v, int64_t v_stride) {
   constexpr int N = Share<T>::kElems;
   using Word = typename Codes<N>::type;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -195,7 +193,7 @@ kv_read_kernel(const Paged p, const int8_t* __restrict__ kc, const __half* __res
         if (e < x.e1) {
           const int64_t at = x.code(p, e);
           q[i] = __ldcs(reinterpret_cast<const Word*>(codes + at));
-          d[i] = __ldg(scales + at / 32);
+          d[i] = scales[at / 32];
         }
       }
 #pragma unroll

@@ -182,3 +182,53 @@ def test_codes_next_to_rounding_borders(dtype):
     for codes, scales in (c[:2], c[2:]):
         assert torch.equal(codes[pg, :, pos % 16].reshape(-1, dim), q)
         assert torch.equal(scales[pg, :, pos % 16].reshape(-1, dim // 32), d)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+def test_calls_in_a_row_see_each_others_rows(dtype):
+    """Two contents written in turn to the same pages by calls queued behind one
+    another, each read back and attended to before the next: every call sees
+    what the one before it wrote, at any place (the kernels overlap in time)."""
+    heads, dim, page, lens = 4, 128, 16, [300, 77, 512]
+    n, B = sum(lens), len(lens)
+    c = capi.kv_cache(sum(-(-m // page) for m in lens), heads, page, dim)
+    at, cols = 0, max(-(-m // page) for m in lens)
+    table = np.full((B, cols), -1, np.int32)
+    for b, m in enumerate(lens):
+        table[b, :-(-m // page)] = at + np.arange(-(-m // page))
+        at += -(-m // page)
+    table, ln, cu = torch.from_numpy(table).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), cu_of(lens)
+    x = [rows(n, heads, dim, dtype, s) * g for s, g in ((1, 1.0), (2, 30.0))]
+    qs = [rows(B, 2 * heads, dim, dtype, s) for s in (3, 4)]
+    cnt = torch.zeros(B * 2 * heads, dtype=torch.int32, device="cuda")
+    ws = torch.empty(capi.lib().nvq_attn_decode_workspace_size(B, 2 * heads, heads, dim), dtype=torch.uint8, device="cuda")
+    want = []
+    for i in range(2):
+        capi.kv_write(c, x[i], x[1 - i], cu, ln, table)
+        torch.cuda.synchronize()
+        kv = capi.kv_read(c, cu, ln, table, n, torch.float32)
+        want.append((*kv, capi.attn_decode(c, qs[i], ln, table, cnt, workspace=ws)))
+        torch.cuda.synchronize()
+    outs = [(torch.empty_like(want[0][0]), torch.empty_like(want[0][1]), torch.empty_like(want[0][2])) for _ in range(100)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+
+    def queue():
+        for r, (k, v, o_) in enumerate(outs):
+            i = r & 1
+            capi.kv_write(c, x[i], x[1 - i], cu, ln, table)
+            capi.kv_read(c, cu, ln, table, n, k=k, v=v)
+            capi.attn_decode(c, qs[i], ln, table, cnt, out=o_, workspace=ws)
+            capi.kv_read(c, cu, ln, table, n, k=k, v=v)
+    queue()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for r, got in enumerate(outs):
+            for a, b in zip(got, want[r & 1]):
+                assert torch.equal(a, b), r
+                a.zero_()
+        if _ == 0:                       # the same from a graph, where the launches follow without a gap
+            with torch.cuda.graph(graph):
+                queue()
+        graph.replay()
+        torch.cuda.synchronize()
