@@ -30,8 +30,8 @@
 // keys) first, dealt to the CTAs forwards and backwards in turn.
 //
 // The running maximum is a reference point only: the maximum of the first step
-// with a finite score, kept while no later step's exponentials add up to more than 2^8 (then none of
-// them is above that).  So a step costs no search for its maximum and no
+// with a finite score, kept while no later step's exponentials add up to more
+// than 2^8 times the reference's (then none of them is above that).  So a step costs no search for its maximum and no
 // rescaling of O; where a row passes the mark, its warp searches, waits for the
 // product before, rescales O and forms the step again.
 //
@@ -68,7 +68,13 @@ constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kCleanWarp = 11;
 constexpr int kRaw = 4;              // V blocks on their way to be cleaned (the ring holds no more)
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
-constexpr float kLazy = 256.0f;       // how far a step's exponentials may add up before the reference moves
+// How far a step's exponentials may add up before the reference moves.  With
+// fp16 they are 2^7 times as large, so that probabilities down to 2^-32 of the
+// reference's count instead of 2^-25: behind one key that stands out, 100000 keys
+// of 2^-25 are 0.3 % of the sum.
+constexpr float kLazy = 256.0f;
+template <bool BF16> constexpr float kShift = BF16 ? 0.0f : 7.0f;          // a power of two
+template <bool BF16> constexpr float kMark = BF16 ? kLazy : 128.0f * kLazy;  // below fp16's 65504
 constexpr float kLarge = 1024.0f;     // exponents from here on are formed as differences first
 
 __device__ unsigned int g_attn_prefill_error_flags = 0;   // bit 0: a wait timed out, bit 1: a bad index
@@ -610,7 +616,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         auto form = [&](auto large) -> float {
           F2 sum0 = f2(0.0f), sum1 = f2(0.0f);
           const bool own = decltype(large)::value && fabsf(ref * c) > kLarge;
-          const F2 m2 = f2(own ? -ref : -0.0f), n2 = f2(own ? 0.0f : -ref * c), c2 = f2(c);
+          const F2 m2 = f2(own ? -ref : -0.0f), n2 = f2(own ? kShift<BF16> : fmaf(-ref, c, kShift<BF16>)), c2 = f2(c);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t p[16];
@@ -635,7 +641,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
         float sum;
         for (int round = 0;; ++round) {
           sum = __any_sync(0xffffffffu, fabsf(ref * c) > kLarge) ? form(Yes{}) : form(No{});
-          const bool grow = !(sum <= kLazy);
+          const bool grow = !(sum <= kMark<BF16>);
           if (round > 0 || !__any_sync(0xffffffffu, grow)) break;
           ptx::tmem_wait_st();       // stores to one place are not kept in order by themselves
           const float top = largest();

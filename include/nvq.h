@@ -530,7 +530,9 @@ size_t nvq_attn_decode_workspace_size(int64_t B, int64_t n_heads, int64_t n_kv_h
  * Keys and values that a query does not see do not reach it, whatever they
  * hold (NaN and infinities included).  Rows of out from cu_q[B] on are left
  * as they were.  Products accumulate in fp32, softmax statistics are fp32,
- * the probabilities are rounded to `dtype` for the product with the values.
+ * the probabilities are rounded to `dtype` for the product with the values
+ * (fp16: as multiples of 2^-31 of the row's largest score's where they are below
+ * 2^-21 of it; bf16 keeps 8 bits of each).
  * A row range outside total_q or total_k raises NVQ_FLAG_BAD_INDEX; the
  * sequence counts as having no keys, its rows inside total_q give zeros.
  * No workspace.  Results do not depend on timing.

@@ -395,3 +395,31 @@ def test_large_and_small_scores_in_one_warp(dtype):
     q[1::3, :, 0] = -60.0
     out = capi.attn_prefill(q, k, v, cu_of([n]), scale=0.5)
     compare(q, k, v, [n], [n], out, dtype, True, 0.5)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("low", [-14.0, -17.5])
+@pytest.mark.parametrize("first", [True, False])
+def test_many_small_probabilities_add_up(dtype, low, first):
+    """One key that stands out before or behind 200000 of small weights, whose
+    values it does not share: what they add up to is the result.  A weight
+    counts down to 2^-32 of the largest with fp16: rounded by up to 2^-32 of
+    it, or by 2^-11 of itself (bf16: 2^-8)."""
+    m, dim, n = 200000, 64, 3
+    rng = np.random.default_rng(2)
+    score = low + rng.uniform(-1, 1, m)
+    score[0 if first else m - n] = 0.0                            # seen by every row
+    k, v = (torch.zeros(m, 1, dim, dtype=dtype, device="cuda") for _ in range(2))
+    k[:, 0, 0] = torch.from_numpy(score).to(dtype).cuda()
+    v[:, 0] = rows(m, 1, dim, dtype, 3)[:, 0] + 3.0
+    v[0 if first else m - n] = 0.0
+    q = torch.zeros(n, 2, dim, dtype=dtype, device="cuda")
+    q[..., 0] = 1.0
+    out = capi.attn_prefill(q, k, v, cu_of([n]), cu_of([m]), scale=1.0)
+    ref, a, e = o.attend_fp64(*[x.double().cpu().numpy() for x in (q, k, v)], 1.0)
+    vmax, half = v.abs().max().item(), 2.0 ** -11 if dtype == torch.float16 else 2.0 ** -8
+    tol = a * (2 * (2.0 ** -18 * e[..., None] + 2.0 ** -21) + (m / 16 + 32) * 2.0 ** -23 + half)
+    tol += m * 2.0 ** -32 * vmax if dtype == torch.float16 else 0
+    tol += half * (np.abs(ref) + tol) + 2.0 ** -25
+    check(out, ref, tol)
+    assert (out > 0).all()
