@@ -84,6 +84,7 @@ SIGNATURES = {
                                         ctypes.c_float, ctypes.c_int, _vp, _c_i64, _vp]),
     "nvq_error_flags": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint), ctypes.c_int]),
     "nvq_debug_stalled_wait": (ctypes.c_int, [ctypes.c_uint64, _vp, _vp]),
+    "nvq_debug_stalled_attn_wait": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_int, _vp, _vp]),
     "nvq_decoder_stack": (ctypes.c_int, [ctypes.POINTER(Linear), _c_i64, _vp, _c_i64,
                                          ctypes.POINTER(_vp), _vp, ctypes.c_size_t, _vp]),
     "nvq_decoder_stack_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Linear), _c_i64]),
@@ -571,6 +572,13 @@ def debug_stalled_wait(limit_ns: int, result: torch.Tensor, stream=None) -> None
     (nvq_debug_stalled_wait); result is a device int32 [2] tensor."""
     _check("nvq_debug_stalled_wait", _lib.nvq_debug_stalled_wait(
         int(limit_ns), _ptr(result), _stream(stream)))
+
+
+def debug_stalled_attn_wait(limit_ns: int, moving: bool, result: torch.Tensor, stream=None) -> None:
+    """Test-only: one wait of the prompt attention that times out, or one that
+    lasts two limits while blocks are counted (nvq_debug_stalled_attn_wait)."""
+    _check("nvq_debug_stalled_attn_wait", _lib.nvq_debug_stalled_attn_wait(
+        int(limit_ns), int(moving), _ptr(result), _stream(stream)))
 
 
 class DecoderStack:

@@ -315,6 +315,59 @@ __device__ __noinline__ bool clean_values(unsigned char* block, int sub_bytes, i
   return any;
 }
 
+// The whole warp waits (one lane then acts; see the prefill GEMM).  The limit
+// holds from the last block that was loaded on: a warp may wait through any
+// number of items that need nothing of it (the cleaner through those without
+// unseen keys, a tile's softmax through those with one tile).  The blocks are
+// counted in `issued`, so the waits still end.  false, and the flag: no block
+// came for the limit, or another warp gave up.
+__device__ __forceinline__ bool counted_wait(uint32_t bar, uint32_t parity, volatile int* issued,
+                                             volatile int* abort_flag, uint64_t limit_ns) {
+  if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+  for (int before = __shfl_sync(0xffffffffu, *issued, 0);;) {
+    const bool got = ptx::mbar_wait_bounded(bar, parity, abort_flag, limit_ns);
+    if (__all_sync(0xffffffffu, got)) return true;
+    const int now = __shfl_sync(0xffffffffu, *issued, 0);
+    if (now == before || __any_sync(0xffffffffu, *abort_flag != 0)) break;
+    before = now;
+  }
+  *abort_flag = 1;
+  atomicOr(&g_attn_prefill_error_flags, 1u);
+  return false;
+}
+
+// Test-only: warp 0 waits as above for a phase that warp 1 completes after two
+// limits, having counted a block every half of one (`moving`), or never.
+__global__ void __launch_bounds__(64) stalled_attn_wait_kernel(uint64_t limit_ns, int moving, int* result) {
+  __shared__ __align__(8) uint64_t bar_s;
+  __shared__ int issued_s, abort_s;
+  volatile int* issued = &issued_s;
+  volatile int* abort_flag = &abort_s;
+  const uint32_t bar = ptx::smem_addr(&bar_s);
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(bar, 1);
+    *issued = *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  const uint64_t t0 = ptx::globaltimer_ns();
+  if (threadIdx.x < 32) {
+    const bool got = counted_wait(bar, 0, issued, abort_flag, limit_ns);
+    const uint64_t us = (ptx::globaltimer_ns() - t0) / 1000;
+    if (threadIdx.x == 0) {
+      result[0] = got ? 1 : 0;
+      result[1] = us > 0x7fffffffull ? 0x7fffffff : static_cast<int>(us);
+    }
+  } else if (moving && threadIdx.x == 32) {
+    for (int r = 1; r <= 4; ++r) {
+      // at most 2^21 sleeps of a microsecond, whatever the clock says
+      for (int i = 0; i < (1 << 21) && ptx::globaltimer_ns() - t0 < r * limit_ns / 2; ++i) __nanosleep(1000);
+      *issued = r;
+    }
+    ptx::mbar_arrive(bar);
+  }
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
@@ -376,26 +429,8 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_cons
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  auto fail = [&]() {
-    *abort_flag = 1;
-    atomicOr(&g_attn_prefill_error_flags, 1u);
-  };
-  // The whole warp waits, one lane acts (see the prefill GEMM).  The limit holds
-  // from the last block that was loaded on: a warp may wait through any number
-  // of items that need nothing of it (the cleaner through those without unseen
-  // keys, a tile's softmax through those with one tile).  The blocks are
-  // counted, so the waits still end.
   auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
-    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(b, parity))) return true;
-    for (int before = __shfl_sync(0xffffffffu, *issued, 0);;) {
-      const bool got = ptx::mbar_wait_bounded(b, parity, abort_flag, kWaitLimitNs);
-      if (__all_sync(0xffffffffu, got)) return true;
-      const int now = __shfl_sync(0xffffffffu, *issued, 0);
-      if (now == before || __any_sync(0xffffffffu, *abort_flag != 0)) break;
-      before = now;
-    }
-    fail();
-    return false;
+    return counted_wait(b, parity, issued, abort_flag, kWaitLimitNs);
   };
   // tensor memory: S (and P) of tile s, buffer b at 128 s + 64 b, O at 256 + 128 s
 
@@ -814,6 +849,11 @@ cudaError_t launch_attn_prefill(const PrefillArgs& a, int dtype, cudaStream_t st
   if (a.head_dim == 64)
     return dtype == NVQ_F16 ? prefill_t<64, false>(a, stream) : prefill_t<64, true>(a, stream);
   return dtype == NVQ_F16 ? prefill_t<128, false>(a, stream) : prefill_t<128, true>(a, stream);
+}
+
+cudaError_t launch_stalled_attn_wait(uint64_t limit_ns, int moving, int* result, cudaStream_t stream) {
+  stalled_attn_wait_kernel<<<1, 64, 0, stream>>>(limit_ns, moving, result);
+  return cudaGetLastError();
 }
 
 cudaError_t attn_prefill_error_flags(bool clear, unsigned int* flags) {

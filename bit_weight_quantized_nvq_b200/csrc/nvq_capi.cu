@@ -532,4 +532,14 @@ nvq_status nvq_debug_stalled_wait(uint64_t limit_ns, int* result, void* stream) 
                                               static_cast<cudaStream_t>(stream)));
 }
 
+nvq_status nvq_debug_stalled_attn_wait(uint64_t limit_ns, int moving, int* result, void* stream) {
+  if (!result) return NVQ_ERR_INVALID_ARG;
+  if (limit_ns < 1000 || limit_ns > 1000000000ull) return NVQ_ERR_INVALID_ARG;
+  if (!aligned16(result)) return NVQ_ERR_MISALIGNED;
+  nvq_status st = check_device();
+  if (st != NVQ_OK) return st;
+  return cuda_status(nvq::launch_stalled_attn_wait(limit_ns, moving, result,
+                                                   static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

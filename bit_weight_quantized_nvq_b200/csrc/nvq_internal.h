@@ -170,6 +170,7 @@ struct PrefillArgs {
   int causal;
 };
 cudaError_t launch_attn_prefill(const PrefillArgs& a, int dtype, cudaStream_t stream);
+cudaError_t launch_stalled_attn_wait(uint64_t limit_ns, int moving, int* result, cudaStream_t stream);
 cudaError_t attn_prefill_error_flags(bool clear, unsigned int* flags);
 
 // The allocation-free GEMM: bytes of its library-owned scratch, and the

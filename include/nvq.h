@@ -584,6 +584,17 @@ nvq_status nvq_error_flags(unsigned int* flags, int clear);
  */
 nvq_status nvq_debug_stalled_wait(uint64_t limit_ns, int* result, void* stream);
 
+/*
+ * nvq_debug_stalled_attn_wait - test-only: the same for the prompt attention's
+ * wait, whose limit starts again whenever a block of keys was loaded.
+ * moving  0: nothing is loaded; the wait gives up after limit_ns, raises
+ *         NVQ_FLAG_ATTN_TIMEOUT and the kernel returns (result[0] = 0).
+ *         Else a block is counted every half limit, and the wait completes
+ *         after two limits (result[0] = 1, no flag).
+ * result and errors: as nvq_debug_stalled_wait.
+ */
+nvq_status nvq_debug_stalled_attn_wait(uint64_t limit_ns, int moving, int* result, void* stream);
+
 /* Linears per decoder layer, in execution order. */
 #define NVQ_STACK_LINEARS 7
 

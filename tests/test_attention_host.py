@@ -178,3 +178,9 @@ def test_binding_refuses_a_workspace_elsewhere_or_with_gaps():
             capi.attn_decode(c, q, i32(2), i32(2, 3), i32(8), workspace=bad)
     with pytest.raises(ValueError, match="CUDA"):            # what is wrong here is the whole call's device
         capi.attn_decode(c, q, i32(2), i32(2, 3), i32(8), workspace=space)
+
+
+def test_the_stalled_wait_is_refused_without_a_place_or_a_limit():
+    for limit, at, st in ((10, p(), ARG), (2 * 10 ** 9, p(), ARG), (10 ** 6, None, ARG), (10 ** 6, p(4), ALIGN)):
+        for moving in (0, 1):
+            assert lib.nvq_debug_stalled_attn_wait(limit, moving, at, None) == st

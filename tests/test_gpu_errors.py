@@ -67,3 +67,21 @@ def test_context_usable_after_a_timeout_and_normal_kernels_raise_nothing():
         assert_within_tolerance(y.cpu().numpy(), y_ref, sa)
     assert capi.error_flags() == 0
     assert np.all(res.cpu().numpy()[:1] == 0)
+
+
+def test_attention_wait_gives_up_only_without_progress():
+    """The prompt attention's wait: nothing loaded for the limit raises its
+    flag; a wait of two limits during which blocks are loaded does not."""
+    torch.cuda.synchronize()
+    capi.error_flags(clear=True)
+    limit_us = 20_000
+    for moving in (False, True, False):
+        res = torch.full((4,), -1, dtype=torch.int32, device="cuda")
+        capi.debug_stalled_attn_wait(limit_us * 1000, moving, res)
+        torch.cuda.synchronize()
+        completed, waited_us = res[:2].cpu().tolist()
+        assert completed == moving
+        # two limits, or one and what the last sleep of 0.5 ms adds; 2 s for a busy machine
+        assert (2 if moving else 1) * limit_us <= waited_us < 2_000_000, waited_us
+        assert capi.error_flags(clear=True) == (0 if moving else capi.FLAG_ATTN_TIMEOUT)
+    assert capi.error_flags() == 0
