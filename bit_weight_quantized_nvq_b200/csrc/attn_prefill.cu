@@ -71,10 +71,11 @@ constexpr uint64_t kWaitLimitNs = 4000000000ull;
 // How far a step's exponentials may add up before the reference moves.  With
 // fp16 they are 2^7 times as large, so that probabilities down to 2^-32 of the
 // reference's count instead of 2^-25: behind one key that stands out, 100000 keys
-// of 2^-25 are 0.3 % of the sum.
+// of 2^-25 are 0.3 % of the sum.  With bf16 they are 2^-24 times as large: the
+// products with its largest values then add up below fp32's largest number.
 constexpr float kLazy = 256.0f;
-template <bool BF16> constexpr float kShift = BF16 ? 0.0f : 7.0f;          // a power of two
-template <bool BF16> constexpr float kMark = BF16 ? kLazy : 128.0f * kLazy;  // below fp16's 65504
+template <bool BF16> constexpr float kShift = BF16 ? -24.0f : 7.0f;                  // a power of two
+template <bool BF16> constexpr float kMark = kLazy * (BF16 ? 0x1p-24f : 0x1p7f);    // fp16: below 65504
 constexpr float kLarge = 1024.0f;     // exponents from here on are formed as differences first
 
 __device__ unsigned int g_attn_prefill_error_flags = 0;   // bit 0: a wait timed out, bit 1: a bad index

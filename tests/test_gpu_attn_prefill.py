@@ -423,3 +423,20 @@ def test_many_small_probabilities_add_up(dtype, low, first):
     tol += half * (np.abs(ref) + tol) + 2.0 ** -25
     check(out, ref, tol)
     assert (out > 0).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("size", [1e-36, 1e-30, 1e30, 2e37, 8e37])
+def test_the_largest_and_smallest_values(dim, size):
+    """bf16 values of up to 3e38 and down to 1e-36: no sum on the way to a
+    weighted mean of them leaves the range."""
+    n, dtype = [300, 70, 1], torch.bfloat16
+    N = sum(n)
+    q, k = rows(N, 4, dim, dtype, 1), rows(N, 2, dim, dtype, 2)
+    v = (rows(N, 2, dim, torch.float32, 3).clamp(-3.5, 3.5) * size).to(dtype)
+    out = capi.attn_prefill(q, k, v, cu_of(n))
+    compare(q, k, v, n, n, out, dtype, True)
+    steps = torch.arange(N, device="cuda").div(64, rounding_mode="floor").view(-1, 1).to(dtype)
+    q[..., 0], k[..., 0] = 1.0, 5.0 * steps           # the reference lags and moves
+    out = capi.attn_prefill(q, k, v, cu_of(n), scale=1.0)
+    compare(q, k, v, n, n, out, dtype, True, 1.0)
