@@ -23,7 +23,8 @@
 // free of bank conflicts.  (One warp issuing TMA boxes for all four was the
 // first form: with pages of 16 tokens, 16 small copies a tile, the copies alone
 // took 66 us for 162 MB; with pages of 128, 127 us for 706 MB.
-// Each warp issuing TMA boxes of its own: 174 us for the 706 MB, against 156.)
+// Each warp issuing TMA boxes of its own: 174 us for the 706 MB, against 156
+// with cp.async then.)
 //
 // Scores (m16n8k16, fp16 operands): A holds the queries, B the codes of 8
 // tokens, which are exact in fp16.  (As code + 128, without the subtraction
@@ -47,9 +48,9 @@
 // with every tile, so the tensor pipe is not what bounds this kernel.
 //
 // Measured, cold L2: 64 sequences of 2048..8192 tokens, 64 over 8 heads of 128,
-// fp16, 156 us (4.5 TB/s); one of 131072, fp32, 84 us (3.4); 24 of 1..6000 with
-// pages of 16, bf16, 53 us (3.0).  Copies alone take 125 us of the 156; the
-// issue slots are 59 % full.
+// fp16, 158 us (4.5 TB/s); one of 131072, fp32, 85 us (3.4); 24 of 1..6000 with
+// pages of 16, bf16, 53 us (3.0); 24 of 1..6000, 64 over 4 heads, fp16, 61 us
+// (1.3).  Copies alone take 125 us of the 158; the issue slots are 61 % full.
 #include <algorithm>
 
 #include <cuda_fp16.h>

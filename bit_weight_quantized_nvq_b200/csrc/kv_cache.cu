@@ -10,10 +10,14 @@
 // x / d32 by IEEE division, rint, clamp; d = fp16(d32)), so a cached row is
 // bit-identical to nvq_quantize_act_q8_0 of it.
 //
-// Both kernels are HBM-bound when they move many rows (write: e + 1.0625
-// bytes per value, read: 1.0625 + e) and launch-bound for a decode step.
-// Measured, cold L2: reading 80052 rows of 8 x 128 as fp16 88 us, 5.7 TB/s;
-// writing 6543 rows of fp16 keys and values, 34.7 us with reading them back.
+// Both kernels have to move e + 1.0625 bytes per value, and are launch-bound for
+// a decode step.  The read of many rows is HBM-bound: 80052 rows of 8 x 128 as
+// fp16, cold L2, 88 us (5.7 TB/s).  The write is not: 7000 such rows take 25 us
+// for 6.6 us of bytes.  A warp's chain of four dependent look-ups, its loads of
+// K, K's quantisation and only then V's loads is hidden by the 24 to 40 other
+// warps that its registers leave room for on an SM (48 to 76 a thread), in two to
+// three waves of CTAs.  Rows of one or two heads leave lanes idle: 12000 rows of
+// 1 x 128 in fp16 are written in 18 us (1.5 us of bytes).
 #include <cstring>
 
 #include <cuda_fp16.h>
@@ -217,9 +221,15 @@ kv_read_kernel(const Paged p, const int8_t* kc, const __half* ks, const int8_t* 
   }
 }
 
-// Warps that share a row: one where there are rows enough to fill the SMs (48
-// warps each), more for a decode step's few rows, as far as a warp still has
-// a piece of K and of V for each of its lanes.
+// Warps that share a row: one where there are rows enough for 48 warps per SM,
+// more for a decode step's few rows, as far as a warp still has a piece of K and
+// of V for each of its lanes.  48 lies between what the two kernels want (24 to
+// 40 warps are resident of the write, 64 of the read); us with 24, 48 and 96:
+//                                   write               read back
+//   4000 rows of 40 x 128, bf16     66   59   60        37   31   31
+//   4000 rows of 40 x 128, fp32     59   57   55        55   45   45
+//   4000 rows of 8 x 128, fp16      16   18   22        14   12   14
+//   7000 rows of 8 x 128, bf16      25   29   39        16   17   21
 Paged paged_of(const nvq_kv_cache& c, const KvBatch& b, int elems) {
   const int64_t width = c.n_kv_heads * c.head_dim;
   int parts = 1;

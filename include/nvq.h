@@ -488,10 +488,13 @@ nvq_status nvq_kv_read(const nvq_kv_cache* cache, void* k, int64_t k_stride, voi
  *       apart: sum_j p_j v_j / sum_j p_j, p_j = exp(scale * q.k_j - max), over
  *       the seq_lens[b] positions of sequence b; zeros where it is 0.
  * scale > 0 and at most 2^64 (customarily 1/sqrt(head_dim)).
- * Products, softmax statistics and sums are fp32; with NVQ_F32 the operands
- * of the products carry at least 22 bits, with the 16-bit types the
+ * Products, softmax statistics and sums are fp32; queries are exact with
+ * the 16-bit types and carry at least 22 bits with NVQ_F32, in either case down
+ * to 2^-39 of the row's largest element; with the 16-bit types the
  * probabilities are rounded to tf32 (fp16's significand, fp32's range) for the
- * product with the values.
+ * product with the values.  A score below fp32's range counts for nothing, one
+ * above it makes its row NaN; value scales that are not finite reach the results
+ * of their block of 32.
  * A length over max_pages * page_size is cut there, a negative one counts as
  * 0, a bad page reads page 0; each raises NVQ_FLAG_BAD_INDEX.
  * counters  device int32 [B * n_heads], 0 before the first call; every
